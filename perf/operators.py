@@ -253,7 +253,7 @@ def _quantise(x):
     """E4M3 codes of the rows x [..., d] and their scales: the least power of two (not under 2^-126) that
     brings the row's largest magnitude to 448 or less."""
     m, e = torch.frexp(x.abs().amax(-1))
-    e = torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-126)
+    e = torch.where(m == 0, -126, torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-126))
     scale = ((e + 127) << 23).view(torch.float32)   # 2^e, exactly
     return (x / scale[..., None]).to(torch.float8_e4m3fn), scale
 
