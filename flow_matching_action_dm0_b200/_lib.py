@@ -30,7 +30,10 @@ EXPORTS = ("rtv_create", "rtv_load_expert", "rtv_set_prefix_kv", "rtv_denoise", 
            "rtv_set_prefix_kv_static", "rtv_draft_create", "rtv_draft_load", "rtv_draft_forward", "rtv_flash_round",
            "rtv_draft_device_status", "rtv_draft_last_error", "rtv_draft_path_name", "rtv_draft_kernel_count",
            "rtv_draft_destroy", "rtv_prefill_create", "rtv_prefill_load", "rtv_prefill_kv", "rtv_prefill_denoise",
-           "rtv_prefill_device_status", "rtv_prefill_last_error", "rtv_prefill_kernel_count", "rtv_prefill_destroy")
+           "rtv_prefill_device_status", "rtv_prefill_last_error", "rtv_prefill_kernel_count", "rtv_prefill_destroy",
+           "rtv_ops_create", "rtv_kv_write", "rtv_kv_read", "rtv_cross_attention", "rtv_cross_attention_workspace",
+           "rtv_shared_attention", "rtv_shared_attention_workspace", "rtv_ops_device_status", "rtv_ops_last_error",
+           "rtv_ops_destroy")
 
 
 class rtv_expert_config(C.Structure):
@@ -65,6 +68,26 @@ class rtv_tensor(C.Structure):
     _fields_ = [
         ("name", C.c_char_p), ("data", C.c_void_p), ("dtype", C.c_int), ("ndim", C.c_int),
         ("shape", C.c_longlong * 4), ("is_device", C.c_int),
+    ]
+
+
+class rtv_kv(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("dtype", C.c_int),
+        ("batch", C.c_int), ("n_tokens", C.c_int), ("n_heads", C.c_int), ("head_dim", C.c_int),
+        ("batch_stride", C.c_longlong), ("token_stride", C.c_longlong), ("head_stride", C.c_longlong),
+        ("scale_batch_stride", C.c_longlong), ("scale_token_stride", C.c_longlong),
+        ("scale_head_stride", C.c_longlong),
+    ]
+
+
+class rtv_queries(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p), ("dtype", C.c_int), ("batch", C.c_int),
+        ("n_tokens", C.c_int), ("n_heads", C.c_int), ("head_dim", C.c_int),
+        ("q_batch_stride", C.c_longlong), ("q_token_stride", C.c_longlong), ("q_head_stride", C.c_longlong),
+        ("out_batch_stride", C.c_longlong), ("out_token_stride", C.c_longlong), ("out_head_stride", C.c_longlong),
+        ("scale", C.c_float),
     ]
 
 
@@ -125,6 +148,23 @@ def load_library(path: str = LIB_PATH):
     lib.rtv_prefill_kernel_count.restype = I
     lib.rtv_prefill_destroy.argtypes = [P]
     lib.rtv_prefill_destroy.restype = None
+    kv, qs, sz = C.POINTER(rtv_kv), C.POINTER(rtv_queries), C.c_size_t
+    lib.rtv_ops_create.argtypes = [I, C.POINTER(P)]
+    lib.rtv_kv_write.argtypes = [P, kv, kv, P, I, P, P]
+    lib.rtv_kv_read.argtypes = [P, kv, I, P, kv, P]
+    lib.rtv_cross_attention.argtypes = [P, qs, kv, P, P, C.c_longlong, P, sz, P]
+    lib.rtv_cross_attention_workspace.argtypes = [P, qs, kv, C.POINTER(sz)]
+    lib.rtv_shared_attention.argtypes = [P, qs, kv, P, kv, P, P, sz, P]
+    lib.rtv_shared_attention_workspace.argtypes = [P, qs, kv, kv, C.POINTER(sz)]
+    lib.rtv_ops_device_status.argtypes = [P, U]
+    lib.rtv_ops_last_error.argtypes = [P]
+    lib.rtv_ops_last_error.restype = C.c_char_p
+    lib.rtv_ops_destroy.argtypes = [P]
+    lib.rtv_ops_destroy.restype = None
+    for n in ("rtv_ops_create", "rtv_kv_write", "rtv_kv_read", "rtv_cross_attention",
+              "rtv_cross_attention_workspace", "rtv_shared_attention", "rtv_shared_attention_workspace",
+              "rtv_ops_device_status"):
+        getattr(lib, n).restype = I
     for n in ("rtv_create", "rtv_load_expert", "rtv_set_prefix_kv", "rtv_set_prefix_kv_static", "rtv_denoise",
               "rtv_verify", "rtv_device_status", "rtv_draft_create", "rtv_draft_load", "rtv_draft_forward",
               "rtv_flash_round", "rtv_draft_device_status", "rtv_prefill_create", "rtv_prefill_load",
@@ -310,3 +350,70 @@ def rtv_prefill_kernel_count(p, n_tokens: int, n_steps: int = 0) -> int:
 def rtv_prefill_destroy(p):
     if p:
         load_library().rtv_prefill_destroy(p)
+
+
+# operators over key/value caches ------------------------------------------------
+
+def rtv_ops_create(device: int = 0):
+    lib = load_library()
+    h = C.c_void_p()
+    s = lib.rtv_ops_create(int(device), C.byref(h))
+    if s != RTV_OK:
+        raise RtvError(s, "rtv_ops_create failed")
+    return h
+
+
+def _ocheck(h, s):
+    if s != RTV_OK:
+        raise RtvError(s, load_library().rtv_ops_last_error(h).decode())
+    return s
+
+
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
+def rtv_kv_write(h, src, cache, start_ptr: int, first: int, count_ptr: int, stream: int = 0):
+    return _ocheck(h, _lib.rtv_kv_write(h, _ref(src), _ref(cache), start_ptr, first, count_ptr, stream))
+
+
+def rtv_kv_read(h, cache, first: int, lens_ptr: int, dst, stream: int = 0):
+    return _ocheck(h, _lib.rtv_kv_read(h, _ref(cache), first, lens_ptr, _ref(dst), stream))
+
+
+def rtv_cross_attention(h, q, kv, lens_ptr, mask_ptr, mask_stride, workspace_ptr, workspace_bytes, stream: int = 0):
+    return _ocheck(h, _lib.rtv_cross_attention(h, _ref(q), _ref(kv), lens_ptr, mask_ptr, mask_stride, workspace_ptr,
+                                               workspace_bytes, stream))
+
+
+def rtv_cross_attention_workspace(h, q, kv) -> int:
+    n = C.c_size_t(0)
+    _ocheck(h, _lib.rtv_cross_attention_workspace(h, _ref(q), _ref(kv), C.byref(n)))
+    return n.value
+
+
+def rtv_shared_attention(h, q, prefix, prefix_mask_ptr, own, own_lens_ptr, workspace_ptr, workspace_bytes,
+                         stream: int = 0):
+    return _ocheck(h, _lib.rtv_shared_attention(h, _ref(q), _ref(prefix), prefix_mask_ptr, _ref(own), own_lens_ptr,
+                                                workspace_ptr, workspace_bytes, stream))
+
+
+def rtv_shared_attention_workspace(h, q, prefix, own) -> int:
+    n = C.c_size_t(0)
+    _ocheck(h, _lib.rtv_shared_attention_workspace(h, _ref(q), _ref(prefix), _ref(own), C.byref(n)))
+    return n.value
+
+
+def rtv_ops_device_status(h):
+    bits = C.c_uint(0)
+    s = load_library().rtv_ops_device_status(h, C.byref(bits))
+    return s, bits.value
+
+
+def rtv_ops_last_error(h) -> str:
+    return load_library().rtv_ops_last_error(h).decode()
+
+
+def rtv_ops_destroy(h):
+    if h:
+        load_library().rtv_ops_destroy(h)

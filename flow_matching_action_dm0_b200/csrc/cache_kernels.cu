@@ -1,0 +1,533 @@
+// Kernels of the operators over key/value caches that run outside the tensor
+// cores: the E4M3 cache's write and read, fp32 attention, and the join of
+// partial attention results.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache_ops.h"
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace rtv {
+
+namespace {
+
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
+  uint32_t h2;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
+}
+// Two fp32 values to E4M3 codes, nearest even (lo in the low byte).
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t t;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t) : "f"(hi), "f"(lo));
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// Cache write: scale = 2^e, e = max(-126, least e with max|x| <= 448 * 2^e);
+// codes = E4M3(x * 2^-e) (exact product, one rounding).  A row is D/8 lanes
+// of 8 elements; the maximum over the row's magnitudes is taken on their bit
+// patterns, which order like the values with infinities and NaN on top.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv_write_kernel(const CacheCall c) {
+  constexpr int LPR = D / 8;                    // lanes of a row
+  constexpr int RPB = 256 / LPR;                // rows of a block
+  const int b = blockIdx.y, o = blockIdx.z;
+  const int lane = threadIdx.x % LPR;
+  int n = c.tokens;
+  if (c.lens) {
+    const int want = c.lens[b];
+    n = min(max(want, 0), c.tokens);
+    if (n != want && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
+  }
+  const long long at0 = (long long)c.first + (c.start ? c.start[b] : 0);
+  const long long rows = (long long)n * c.heads;
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < rows; r0 += (long long)gridDim.x * RPB) {
+    const long long r = r0 + threadIdx.x / LPR;
+    const int t = (int)(r / c.heads), h = (int)(r - (long long)t * c.heads);
+    const bool real = r < rows;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (real) {
+      const T* src = reinterpret_cast<const T*>(c.rows.base + o * c.rows.outer_bytes) + b * c.rows.sb + t * c.rows.st +
+                     h * c.rows.sh + lane * 8;
+      if (sizeof(T) == 2) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(w[i] << 16);
+          x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      } else {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(src)), w = __ldcs(reinterpret_cast<const float4*>(src) + 1);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+      }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int k = LPR / 2; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+    if (!real) continue;
+    const long long at = at0 + t;
+    if (at < 0 || at >= c.capacity) {
+      if (lane == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
+      continue;
+    }
+    // 448 = 1.75 * 2^8
+    const int e = max(-126, (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+    const bool finite = top < 0x7F800000u;
+    const float inv = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+    uint2 codes = make_uint2(0u, 0u);
+    if (finite) {
+      codes.x = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv) | f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+      codes.y = f32x2_to_e4m3x2(x[4] * inv, x[5] * inv) | f32x2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+    }
+    uint8_t* dst = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + at * c.cache.st + h * c.cache.sh;
+    *reinterpret_cast<uint2*>(dst + lane * 8) = codes;
+    if (lane == 0) {
+      float* f = reinterpret_cast<float*>(reinterpret_cast<char*>(c.cache.scales) + o * c.cache.scales_outer);
+      f[b * c.cache.fb + at * c.cache.ft + h * c.cache.fh] =
+          finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+    }
+  }
+}
+
+// Cache read: code * scale, rounded once.  A row is D/16 lanes of 16 codes.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv_read_kernel(const CacheCall c) {
+  constexpr int LPR = D / 16;
+  constexpr int RPB = 256 / LPR;
+  const int b = blockIdx.y, o = blockIdx.z;
+  const int lane = threadIdx.x % LPR;
+  int n = c.capacity;   // valid cache tokens
+  if (c.lens) {
+    const int want = c.lens[b];
+    n = min(max(want, 0), c.capacity);
+    if (n != want && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
+  }
+  const long long rows = (long long)c.tokens * c.heads;
+  for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR; r < rows; r += (long long)gridDim.x * RPB) {
+    const int t = (int)(r / c.heads), h = (int)(r - (long long)t * c.heads);
+    const long long at = (long long)c.first + t;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    if (at < n) {
+      const uint8_t* src = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + at * c.cache.st + h * c.cache.sh;
+      const float* f = reinterpret_cast<const float*>(reinterpret_cast<const char*>(c.cache.scales) + o * c.cache.scales_outer);
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
+      const float s = f[b * c.cache.fb + at * c.cache.ft + h * c.cache.fh];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 p = e4m3x2_to_f32x2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+        x[2 * i] = p.x * s;
+        x[2 * i + 1] = p.y * s;
+      }
+    }
+    T* dst = reinterpret_cast<T*>(c.rows.base + o * c.rows.outer_bytes) + b * c.rows.sb + t * c.rows.st +
+             h * c.rows.sh + lane * 16;
+    if (sizeof(T) == 2) {
+      uint4 u[2];
+      uint32_t* w = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      reinterpret_cast<uint4*>(dst)[0] = u[0];
+      reinterpret_cast<uint4*>(dst)[1] = u[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32 attention: BM rows against tiles of 64 keys, 256 threads as 16 x 16;
+// thread (ty, tx) holds rows ty + 16 i, keys tx + 16 j of the scores and
+// columns 4 tx + 64 c of the output.  One pass over the keys with the running
+// maximum (base 2) and sum of each row.  Hidden keys score -inf and their
+// values are read as zeros, whatever they hold.
+// ---------------------------------------------------------------------------
+constexpr int kKeys = 64;
+
+__host__ __device__ constexpr int attn_f32_smem(int bm, int d) {
+  return 4 * (bm * (d + 4) + kKeys * (d + 4) + kKeys * d + bm * (kKeys + 4) + kKeys);
+}
+
+template <typename QT>
+__device__ __forceinline__ float4 load4(const QT* p) {
+  if (sizeof(QT) == 4) return *reinterpret_cast<const float4*>(p);
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xFFFF0000u));
+}
+template <typename QT>
+__device__ __forceinline__ void store4(QT* p, float4 v) {
+  if (sizeof(QT) == 4) *reinterpret_cast<float4*>(p) = v;
+  else *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
+}
+// Four elements of a key or value row: QT values, or E4M3 codes times the row's scale.
+template <typename QT>
+__device__ __forceinline__ float4 load_kv4(const void* base, const float* scales, bool f8, long long off, long long foff) {
+  if (!f8) return load4(reinterpret_cast<const QT*>(base) + off);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) + off);
+  const float s = scales[foff];
+  const float2 a = e4m3x2_to_f32x2(w & 0xFFFFu), b = e4m3x2_to_f32x2(w >> 16);
+  return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+}
+
+template <typename QT, int D, int BM>
+__global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ AttnCall c) {
+  constexpr int TM = BM / 16, LD = D + 4, LP = kKeys + 4, C4 = D / 4;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + BM * LD;
+  float* Vs = Ks + kKeys * LD;
+  float* Ps = Vs + kKeys * D;
+  float* Ok = Ps + BM * LP;       // 1: the tile's key is seen
+  const AttnUnit u = attn_unit(c);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+
+  for (int i = tid; i < BM * C4; i += 256) {
+    const int r = i / C4, d = (i - r * C4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < u.nrows) {
+      const long long row = u.row0 + r;
+      const long long b = row / c.plan.rows_b;
+      const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, g = rr - t * c.group;
+      v = load4(reinterpret_cast<const QT*>(c.q) + b * c.qb + t * c.qt + (long long)(u.kvh * c.group + g) * c.qh + d);
+    }
+    *reinterpret_cast<float4*>(Qs + r * LD + d) = v;
+  }
+
+  float m[TM], l[TM];
+  float4 acc[TM][D / 64];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) acc[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+
+  for (int tile = u.t0; tile < u.t1; ++tile) {
+    const bool pre = tile < u.n0;
+    const KvSource& s = pre ? c.pre : c.own;
+    const bool f8 = pre ? c.pre_f8 : c.own_f8;
+    const int bb = pre ? 0 : u.b;
+    const int k0 = (pre ? tile : tile - u.n0) * kKeys;
+    const int nk = min(kKeys, (pre ? u.len0 : u.len1) - k0);
+    __syncthreads();
+    if (tid < kKeys) Ok[tid] = tid < nk && (!s.mask || s.mask[bb * s.mask_sb + k0 + tid]) ? 1.f : 0.f;
+    __syncthreads();
+    for (int i = tid; i < kKeys * C4; i += 256) {
+      const int r = i / C4, d = (i - r * C4) * 4;
+      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      if (Ok[r] != 0.f) {
+        const long long off = bb * s.sb + (long long)(k0 + r) * s.st + u.kvh * s.sh + d;
+        const long long foff = bb * s.fb + (long long)(k0 + r) * s.ft + u.kvh * s.fh;
+        kv = load_kv4<QT>(s.k, s.ks, f8, off, foff);
+        vv = load_kv4<QT>(s.v, s.vs, f8, off, foff);
+      }
+      *reinterpret_cast<float4*>(Ks + r * LD + d) = kv;
+      *reinterpret_cast<float4*>(Vs + r * D + d) = vv;
+    }
+    __syncthreads();
+    float sc[TM][4];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 qv[TM], kv[4];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * LD + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sc[i][j] = fmaf(qv[i].x, kv[j].x,
+                          fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, sc[i][j]))));
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sc[i][j] = Ok[tx + 16 * j] != 0.f ? sc[i][j] * c.scale_log2 : -INFINITY;
+        top = fmaxf(top, sc[i][j]);
+      }
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m[i] - base);   // 0 before the row's first key
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(sc[i][j] - base);
+        Ps[(ty + 16 * i) * LP + tx + 16 * j] = p;
+        sum += p;
+      }
+      l[i] = l[i] * corr + sum;   // this lane's share of the row's sum
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        acc[i][k].x *= corr;
+        acc[i][k].y *= corr;
+        acc[i][k].z *= corr;
+        acc[i][k].w *= corr;
+      }
+    }
+    __syncwarp();   // a row's weights are written and read by the same half-warp
+#pragma unroll 2
+    for (int k4 = 0; k4 < kKeys; k4 += 4) {
+      float4 p[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * LP + k4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int cc = 0; cc < D / 64; ++cc) {
+          const float4 v = *reinterpret_cast<const float4*>(Vs + (k4 + kk) * D + 64 * cc + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+            acc[i][cc].x = fmaf(w, v.x, acc[i][cc].x);
+            acc[i][cc].y = fmaf(w, v.y, acc[i][cc].y);
+            acc[i][cc].z = fmaf(w, v.z, acc[i][cc].z);
+            acc[i][cc].w = fmaf(w, v.w, acc[i][cc].w);
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
+    const int r = ty + 16 * i;
+    if (r >= u.nrows) continue;
+    const long long row = u.row0 + r;
+    if (c.plan.n_slots > 1) {
+      const long long pr = part_row(c, u, row);
+      // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
+      const float mo = l[i] != l[i] ? INFINITY : l[i] == 0.f ? -INFINITY : m[i];
+      if (tx == 0) *reinterpret_cast<float2*>(c.part_ml + pr * 2) = make_float2(mo, l[i]);
+      if (mo == -INFINITY) continue;   // the join does not read an empty part
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) *reinterpret_cast<float4*>(c.part_o + pr * D + 64 * k + 4 * tx) = acc[i][k];
+      continue;
+    }
+    const long long b = row / c.plan.rows_b;
+    const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, h = u.kvh * c.group + rr - t * c.group;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    QT* dst = reinterpret_cast<QT*>(c.out) + b * c.ob + t * c.ot + h * c.oh + 4 * tx;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      store4(dst + 64 * k, make_float4(acc[i][k].x * inv, acc[i][k].y * inv, acc[i][k].z * inv, acc[i][k].w * inv));
+    if (c.lse && tx == 0)
+      c.lse[(b * c.Tq + t) * c.Hq + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+  }
+}
+
+// Join of a row's partial results: out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,
+// slots in order; a warp per row.  Empty parts (m = -inf) are not read.
+template <typename QT, int D>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnCall c) {
+  constexpr int V = D >= 128 ? 4 : 2, NC = D / (32 * V);   // elements of a lane's load, loads of a lane
+  const long long rows = (long long)c.B * c.plan.rows_b;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int kvh = blockIdx.y, lane = threadIdx.x & 31, n = c.plan.n_slots;
+  ptx::pdl_wait();
+  if (row >= rows) return;
+  const long long base = (long long)kvh * n * rows + row;
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, c.part_ml[(base + k * rows) * 2]);
+  top = warp_max(top);
+  float acc[NC][V] = {};
+  float sum = 0.f;
+  if (top != -INFINITY) {
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < n) ml = *reinterpret_cast<const float2*>(c.part_ml + (base + (k0 + lane) * rows) * 2);
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+      sum += ml.x == -INFINITY ? 0.f : w * ml.y;
+      const int kn = min(32, n - k0);
+#pragma unroll 4
+      for (int k = 0; k < kn; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k), mk = __shfl_sync(0xffffffffu, ml.x, k);
+        if (mk == -INFINITY) continue;
+        const float* src = c.part_o + (base + (k0 + k) * rows) * D + lane * V;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          float v[V];
+          if (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + 32 * V * i);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src + 32 * V * i);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[i][e] = fmaf(wk, v[e], acc[i][e]);
+        }
+      }
+    }
+    sum = warp_sum(sum);
+  }
+  const long long b = row / c.plan.rows_b;
+  const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, h = kvh * c.group + rr - t * c.group;
+  const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+  QT* dst = reinterpret_cast<QT*>(c.out) + b * c.ob + t * c.ot + h * c.oh + lane * V;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (sizeof(QT) == 4) {
+#pragma unroll
+      for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(dst) + 32 * V * i + e) =
+            make_float2(acc[i][e] * inv, acc[i][e + 1] * inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + 32 * V * i + e) = ptx::pack_bf16x2(acc[i][e] * inv, acc[i][e + 1] * inv);
+    }
+  }
+  if (c.lse && lane == 0)
+    c.lse[(b * c.Tq + t) * c.Hq + h] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename QT, int D, int BM>
+cudaError_t launch_f32(const AttnCall& c, cudaStream_t st) {
+  const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + (long long)c.B * c.plan.tiles_e * c.plan.ne), c.Hkv);
+  attn_f32_kernel<QT, D, BM><<<grid, 256, attn_f32_smem(BM, D), st>>>(c);
+  return cudaGetLastError();
+}
+
+template <typename QT, int D>
+cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)c.B * c.plan.rows_b + 7) / 8), c.Hkv);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<QT, D>, c);
+}
+
+template <typename QT, int D>
+cudaError_t launch_all(const AttnCall& c, cudaStream_t st) {
+  cudaError_t e = c.plan.bm == 16 ? launch_f32<QT, D, 16>(c, st) : launch_f32<QT, D, 64>(c, st);
+  if (e == cudaSuccess && c.plan.n_slots > 1) e = launch_combine<QT, D>(c, st);
+  return e;
+}
+
+template <typename QT, int D, int BM>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(attn_f32_kernel<QT, D, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              attn_f32_smem(BM, D));
+}
+
+template <typename T, int D>
+cudaError_t write_d(const CacheCall& c, const dim3& grid, cudaStream_t st) {
+  kv_write_kernel<T, D><<<grid, 256, 0, st>>>(c);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t read_d(const CacheCall& c, const dim3& grid, cudaStream_t st) {
+  kv_read_kernel<T, D><<<grid, 256, 0, st>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const CacheCall& c, cudaStream_t st) {
+  const long long rpb = 2048 / c.dim, rows = (long long)c.tokens * c.heads;
+  const dim3 grid((unsigned)std::min((rows + rpb - 1) / rpb, 65535LL), c.batch, c.outer);
+  if (c.bf16) return c.dim == 64    ? write_d<__nv_bfloat16, 64>(c, grid, st)
+                     : c.dim == 128 ? write_d<__nv_bfloat16, 128>(c, grid, st)
+                                    : write_d<__nv_bfloat16, 256>(c, grid, st);
+  return c.dim == 64 ? write_d<float, 64>(c, grid, st)
+         : c.dim == 128 ? write_d<float, 128>(c, grid, st) : write_d<float, 256>(c, grid, st);
+}
+
+cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
+  const long long rpb = 4096 / c.dim, rows = (long long)c.tokens * c.heads;
+  const dim3 grid((unsigned)std::min((rows + rpb - 1) / rpb, 65535LL), c.batch, c.outer);
+  if (c.bf16) return c.dim == 64    ? read_d<__nv_bfloat16, 64>(c, grid, st)
+                     : c.dim == 128 ? read_d<__nv_bfloat16, 128>(c, grid, st)
+                                    : read_d<__nv_bfloat16, 256>(c, grid, st);
+  return c.dim == 64 ? read_d<float, 64>(c, grid, st)
+         : c.dim == 128 ? read_d<float, 128>(c, grid, st) : read_d<float, 256>(c, grid, st);
+}
+
+AttnPlan plan_attention(const AttnCall& c, int num_sms) {
+  AttnPlan p{};
+  p.rows_b = c.Tq * c.group;
+  p.kt = kKeys;
+  p.bm = p.rows_b <= 16 ? 16 : 64;
+  const int tb = (p.rows_b + p.bm - 1) / p.bm;
+  // Rows of several elements share a tile (and its pass over the prefix) when
+  // one element's rows would leave most of it empty.
+  const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= p.bm / 2;
+  auto split = [&](long long units, int keys) {
+    const int tiles = (keys + p.kt - 1) / p.kt;
+    const long long want = units * c.Hkv >= 2 * num_sms ? 1 : (2LL * num_sms) / (units * c.Hkv);
+    return (int)std::max(1LL, std::min<long long>({want, tiles, 64}));
+  };
+  if (stack) {
+    p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm - 1) / p.bm);
+    p.ns = split(p.tiles_s, c.pre.len);
+  }
+  p.prefix_in_elem = c.pre.len > 0 && !stack;
+  if (!stack || c.own.len > 0) {
+    p.tiles_e = tb;
+    p.ne = split((long long)c.B * tb, c.own.len + (p.prefix_in_elem ? c.pre.len : 0));
+  }
+  p.n_slots = p.ns + p.ne;
+  return p;
+}
+
+size_t attention_workspace(const AttnCall& c) {
+  if (c.plan.n_slots <= 1) return 0;
+  return (size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * (size_t)(c.D + 2) * 4;
+}
+
+cudaError_t configure_attention() {
+  cudaError_t e = cudaSuccess;
+  auto chain = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
+  chain(set_smem<float, 64, 16>());
+  chain(set_smem<float, 64, 64>());
+  chain(set_smem<float, 128, 16>());
+  chain(set_smem<float, 128, 64>());
+  chain(set_smem<float, 256, 16>());
+  chain(set_smem<float, 256, 64>());
+  chain(set_smem<__nv_bfloat16, 64, 16>());
+  chain(set_smem<__nv_bfloat16, 64, 64>());
+  chain(set_smem<__nv_bfloat16, 128, 16>());
+  chain(set_smem<__nv_bfloat16, 128, 64>());
+  chain(set_smem<__nv_bfloat16, 256, 16>());
+  chain(set_smem<__nv_bfloat16, 256, 64>());
+  return e;
+}
+
+cudaError_t launch_attention(AttnCall& c, void* workspace, int num_sms, cudaStream_t st) {
+  (void)num_sms;
+  c.part_o = (float*)workspace;
+  c.part_ml = c.part_o + (size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * c.D;
+  if (c.bf16)
+    return c.D == 64    ? launch_all<__nv_bfloat16, 64>(c, st)
+           : c.D == 128 ? launch_all<__nv_bfloat16, 128>(c, st)
+                        : launch_all<__nv_bfloat16, 256>(c, st);
+  return c.D == 64 ? launch_all<float, 64>(c, st) : c.D == 128 ? launch_all<float, 128>(c, st) : launch_all<float, 256>(c, st);
+}
+
+}  // namespace rtv

@@ -1,0 +1,156 @@
+// Operators over key/value caches: what the entry points (cache_ops.cu), the
+// fp32 kernels and the tensor-core attention (cache_attn_tc.cu) share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/rtv.h"
+
+namespace rtv {
+
+// Keys and values one attention call reads: one prefix for every batch
+// element, or each element's own tokens.
+struct KvSource {
+  const void *k, *v;
+  const float *ks, *vs;        // E4M3 only
+  long long sb, st, sh;        // element strides: batch, token, head
+  long long fb, ft, fh;        // scale strides
+  int len;                     // tokens (0: the source is absent)
+  const int* lens;             // [B] valid tokens, or nullptr
+  const uint8_t* mask;         // key mask (row b at b * mask_sb), or nullptr
+  long long mask_sb;
+};
+
+// How an attention call is split over CTAs.  A "row" is one (query token,
+// query head) of a KV head's group: row r of element b is token r / group,
+// head kvh * group + r % group.  Stacked units take 128 (tensor cores) or
+// BM (fp32) consecutive rows of the whole batch over a range of the prefix;
+// element units take rows of one element over a range of [prefix ; own keys]
+// (prefix_in_elem) or of its own keys.  Each row has n_slots partial results
+// (slot = range), joined by combine_kernel when there is more than one.
+struct AttnPlan {
+  int bm;                      // rows of a unit
+  int kt;                      // keys of a tile
+  int rows_b;                  // rows of one element: query tokens * group
+  int tiles_s, ns;             // stacked units: row tiles, key ranges (0: none)
+  int tiles_e, ne;             // element units: row tiles per element, key ranges (0: none)
+  int prefix_in_elem;          // element units read the prefix too
+  int n_slots;                 // ns + ne
+};
+
+struct AttnCall {
+  const void* q;
+  void* out;
+  float* lse;
+  long long qb, qt, qh;        // element strides of q: batch, token, head
+  long long ob, ot, oh;
+  int out_tiled_rows;          // > 0: out is the tiled GEMM input of that many block rows (bf16)
+  int bf16;                    // queries and output: 1 bf16, 0 fp32
+  int B, Tq, Hq, Hkv, group, D;
+  float scale_log2;            // scale * log2(e)
+  KvSource pre, own;
+  int pre_f8, own_f8;
+  AttnPlan plan;
+  float* part_o;               // [Hkv][n_slots][B * rows_b][D] unnormalised rows (n_slots > 1)
+  float* part_ml;              // [Hkv][n_slots][B * rows_b][2] their maximum (base 2) and sum
+  unsigned* status;
+  long long timeout_ns;
+};
+
+// Chooses the split for a call whose shape fields are set.
+AttnPlan plan_attention(const AttnCall& c, int num_sms);
+// Bytes of the partial results of a planned call.
+size_t attention_workspace(const AttnCall& c);
+// Enqueues a planned call; workspace as above.
+cudaError_t launch_attention(AttnCall& c, void* workspace, int num_sms, cudaStream_t st);
+// Sets the kernels' attributes on the current device (outside any capture).
+cudaError_t configure_attention();
+
+// One tensor of rows [outer][batch][token][head][D] for the cache kernels;
+// strides in elements, the outer index (keys, values, or layers of both)
+// in bytes, so that it can step between two allocations.
+struct RowsView {
+  char* base;
+  long long outer_bytes;
+  long long sb, st, sh;
+};
+struct CacheView {
+  uint8_t* codes;
+  float* scales;
+  long long codes_outer, scales_outer;   // bytes
+  long long sb, st, sh, fb, ft, fh;
+};
+struct CacheCall {
+  RowsView rows;               // fp32 or bf16 rows: source of a write, destination of a read
+  CacheView cache;
+  int outer, batch, tokens, heads, dim, capacity, bf16;
+  int first;
+  const int* start;            // write: [batch] or nullptr
+  const int* lens;             // write: count; read: valid tokens ([batch] or nullptr)
+  unsigned* status;
+};
+cudaError_t launch_kv_write(const CacheCall& c, cudaStream_t st);
+cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st);
+
+// What one CTA of an attention kernel computes.
+struct AttnUnit {
+  int kvh, b;                  // b: the element of an element unit (0 for a stacked one)
+  long long row0;              // first row in [0, B * rows_b)
+  int nrows, slot;
+  int t0, t1;                  // its tiles of the list [prefix tiles ; own tiles]
+  int n0;                      // prefix tiles in the list
+  int len0, len1;              // keys of the two sources it may read
+};
+
+__device__ __forceinline__ int valid_len(const KvSource& s, int b, unsigned* status) {
+  if (!s.lens) return s.len;
+  const int n = s.lens[b];
+  if ((n < 0 || n > s.len) && threadIdx.x == 0) atomicOr(status, RTV_DEV_BOUNDS);
+  return min(max(n, 0), s.len);
+}
+
+__device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
+  const AttnPlan& p = c.plan;
+  AttnUnit u;
+  u.kvh = blockIdx.y;
+  long long x = blockIdx.x;
+  const long long stacked = (long long)p.tiles_s * p.ns;
+  int split, nsplit;
+  if (x < stacked) {
+    const int tile = (int)(x % p.tiles_s);
+    split = (int)(x / p.tiles_s);
+    nsplit = p.ns;
+    u.slot = split;
+    u.b = 0;
+    u.row0 = (long long)tile * p.bm;
+    u.nrows = (int)min((long long)p.bm, (long long)c.B * p.rows_b - u.row0);
+    u.len0 = valid_len(c.pre, 0, c.status);
+    u.len1 = 0;
+  } else {
+    x -= stacked;
+    const int tile = (int)(x % p.tiles_e);
+    x /= p.tiles_e;
+    split = (int)(x % p.ne);
+    nsplit = p.ne;
+    u.b = (int)(x / p.ne);
+    u.slot = p.ns + split;
+    u.row0 = (long long)u.b * p.rows_b + (long long)tile * p.bm;
+    u.nrows = min(p.bm, p.rows_b - tile * p.bm);
+    u.len0 = p.prefix_in_elem ? valid_len(c.pre, 0, c.status) : 0;
+    u.len1 = valid_len(c.own, u.b, c.status);
+  }
+  u.n0 = (u.len0 + p.kt - 1) / p.kt;
+  const long long n = u.n0 + (u.len1 + p.kt - 1) / p.kt;
+  u.t0 = (int)(n * split / nsplit);
+  u.t1 = (int)(n * (split + 1) / nsplit);
+  return u;
+}
+
+// Where a row's partial result goes.
+__device__ __forceinline__ long long part_row(const AttnCall& c, const AttnUnit& u, long long row) {
+  return ((long long)u.kvh * c.plan.n_slots + u.slot) * ((long long)c.B * c.plan.rows_b) + row;
+}
+
+}  // namespace rtv

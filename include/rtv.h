@@ -397,6 +397,125 @@ int rtv_prefill_kernel_count(rtv_prefill* p, int n_tokens, int n_steps);
  * those was destroyed. */
 void rtv_prefill_destroy(rtv_prefill* p);
 
+/* ------------------------------------------------------------------------
+ * Operators over key/value caches: tokens quantised to FP8 E4M3 as they are
+ * written and read back, cross attention of queries to cached states of
+ * another length, and attention of a batch to one shared prefix.
+ *
+ * Every array is device memory of the handle's GPU; the last index of each
+ * (head_dim) is dense, the others have strides, in elements.  Base addresses
+ * and strides of arrays with a head_dim index are multiples of 16 bytes
+ * (otherwise RTV_ERR_ARG); those of scales, lengths and masks are free.
+ * head_dim is 64, 128 or 256 (otherwise RTV_ERR_UNSUPPORTED).  Null pointers,
+ * host memory and another GPU's memory return RTV_ERR_ARG, contradictory
+ * sizes RTV_ERR_SHAPE; nothing is enqueued on an error.  The calls allocate
+ * nothing and keep nothing between them, so they may be captured into a
+ * CUDA graph and run on several streams at once, as long as each has a
+ * workspace of its own; calls on one handle must not run concurrently from
+ * several host threads.  Outputs must not overlap inputs.
+ * ------------------------------------------------------------------------ */
+typedef struct rtv_ops rtv_ops;
+
+/*
+ * Keys and values of `batch` elements: n_tokens x n_heads rows of head_dim
+ * each, both with the same strides.  dtype RTV_F32, RTV_BF16, or
+ * RTV_FP8_E4M3: codes with one fp32 scale per (element, token, head) in
+ * k_scale and v_scale (scale strides in elements; NULL otherwise), where a
+ * row stands for code * scale.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int dtype;
+  int batch, n_tokens, n_heads, head_dim;
+  long long batch_stride, token_stride, head_stride;
+  long long scale_batch_stride, scale_token_stride, scale_head_stride;
+} rtv_kv;
+
+/*
+ * Queries and where their attention goes: q and out [batch][n_tokens]
+ * [n_heads][head_dim] in dtype (RTV_F32 or RTV_BF16); lse, when not NULL, is
+ * dense [batch][n_tokens][n_heads] fp32: the natural logarithm of the sum of
+ * exp(score).  score = scale * q.k.  n_heads is a multiple of the keys'
+ * heads; query head h reads key/value head h / (n_heads / kv heads).  A query
+ * that sees no key gives out = 0 and lse = -infinity.
+ */
+typedef struct {
+  const void* q;
+  void* out;
+  float* lse;
+  int dtype;
+  int batch, n_tokens, n_heads, head_dim;
+  long long q_batch_stride, q_token_stride, q_head_stride;
+  long long out_batch_stride, out_token_stride, out_head_stride;
+  float scale;
+} rtv_queries;
+
+/* Create a handle on CUDA device `cuda_device` (RTV_ERR_CUDA for a bad
+ * device).  *out is NULL on failure. */
+rtv_status rtv_ops_create(int cuda_device, rtv_ops** out);
+
+/* Quantise src (RTV_F32 or RTV_BF16) into the E4M3 cache as it is written:
+ * token t of element b goes to cache token start[b] + first + t (start NULL:
+ * first + t), for t < count[b] (count NULL: every token).  Per row x: scale =
+ * the least power of two, 2^-126 or more, with max|x| <= 448 * scale; code =
+ * x / scale rounded to nearest even.  The division is exact, so a row takes
+ * one rounding, and code * scale is exact in bf16 and fp32.  A row that holds
+ * a NaN or an infinity gets scale NaN.  Other cache tokens, and tokens from
+ * count[b] on, are left as they are.  start, count: device int32 [batch].
+ * Tokens that fall outside the cache are not written and raise
+ * RTV_DEV_BOUNDS; a count outside [0, n_tokens] is clamped and raises it.
+ * Two tokens of one call never share a place; calls that write the same
+ * places at once race. */
+rtv_status rtv_kv_write(rtv_ops* ops, const rtv_kv* src, const rtv_kv* cache, const int* start, int first,
+                        const int* count, rtv_stream stream);
+
+/* Read cache tokens first .. first + dst->n_tokens - 1 of every element into
+ * dst (RTV_F32 or RTV_BF16): code * scale, rounded once to dst's dtype (exact
+ * in bf16 when the scale is a power of two).  Tokens at or past lens[b]
+ * (device int32 [batch], or NULL) read as zeros; so do those that a length
+ * outside [0, cache tokens] cannot mean (it is clamped, RTV_DEV_BOUNDS). */
+rtv_status rtv_kv_read(rtv_ops* ops, const rtv_kv* cache, int first, const int* lens, const rtv_kv* dst,
+                       rtv_stream stream);
+
+/* Attention of element b's queries to element b's keys (kv->batch ==
+ * q->batch): keys t < lens[b] (device int32 [batch]; NULL: every token;
+ * values outside [0, n_tokens] are clamped and raise RTV_DEV_BOUNDS) whose
+ * mask[b * mask_stride + t] is not 0 (device bytes; NULL: every key).  kv is
+ * in the queries' dtype or RTV_FP8_E4M3.  What hidden keys and values hold is
+ * never used, NaN and infinities included.  bf16 queries: products on the
+ * tensor cores with fp32 sums, softmax weights rounded to bf16; fp32 queries:
+ * fp32 throughout.  workspace: at least rtv_cross_attention_workspace bytes,
+ * 256-byte aligned (NULL when that is 0), in use until the call's work is
+ * done. */
+rtv_status rtv_cross_attention(rtv_ops* ops, const rtv_queries* q, const rtv_kv* kv, const int* lens,
+                               const unsigned char* mask, long long mask_stride, void* workspace,
+                               size_t workspace_bytes, rtv_stream stream);
+rtv_status rtv_cross_attention_workspace(rtv_ops* ops, const rtv_queries* q, const rtv_kv* kv, size_t* bytes);
+
+/* Attention of every element to one shared prefix and to its own keys: keys
+ * of `prefix` (batch 1, the queries' dtype or RTV_FP8_E4M3) whose
+ * prefix_mask[t] is not 0 (device bytes [n_tokens], or NULL), and element
+ * b's keys t < own_lens[b] of `own` (the queries' dtype, batch == q->batch;
+ * NULL: none; own_lens as lens above).  Queries of several elements read the
+ * prefix together.  Otherwise as rtv_cross_attention. */
+rtv_status rtv_shared_attention(rtv_ops* ops, const rtv_queries* q, const rtv_kv* prefix,
+                                const unsigned char* prefix_mask, const rtv_kv* own, const int* own_lens,
+                                void* workspace, size_t workspace_bytes, rtv_stream stream);
+rtv_status rtv_shared_attention_workspace(rtv_ops* ops, const rtv_queries* q, const rtv_kv* prefix,
+                                          const rtv_kv* own, size_t* bytes);
+
+/* As rtv_device_status, for the handle's calls. */
+rtv_status rtv_ops_device_status(rtv_ops* ops, unsigned* bits);
+
+/* Last error message of the handle (never NULL). */
+const char* rtv_ops_last_error(rtv_ops* ops);
+
+/* Release the handle.  NULL is accepted. */
+void rtv_ops_destroy(rtv_ops* ops);
+
 #ifdef __cplusplus
 }
 #endif

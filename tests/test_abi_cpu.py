@@ -98,3 +98,36 @@ def test_invalid_draft_config_is_refused_before_device_use(field, value):
     d = C.c_void_p()
     assert L.load_library().rtv_draft_create(C.byref(cfg), 0, C.byref(d)) == L.RTV_ERR_ARG
     assert not d.value
+
+
+def test_cache_operator_calls_are_refused_without_a_handle():
+    lib = L.load_library()
+    h = C.c_void_p()
+    assert lib.rtv_ops_create(0, None) == L.RTV_ERR_ARG
+    assert lib.rtv_ops_create(-1, C.byref(h)) == L.RTV_ERR_CUDA and not h.value
+    kv, q, n = L.rtv_kv(), L.rtv_queries(), C.c_size_t(7)
+    assert lib.rtv_kv_write(None, C.byref(kv), C.byref(kv), None, 0, None, None) == L.RTV_ERR_ARG
+    assert lib.rtv_kv_read(None, C.byref(kv), 0, None, C.byref(kv), None) == L.RTV_ERR_ARG
+    assert lib.rtv_cross_attention(None, C.byref(q), C.byref(kv), None, None, 0, None, 0, None) == L.RTV_ERR_ARG
+    assert lib.rtv_cross_attention_workspace(None, C.byref(q), C.byref(kv), C.byref(n)) == L.RTV_ERR_ARG
+    assert lib.rtv_shared_attention(None, C.byref(q), C.byref(kv), None, None, None, None, 0, None) == L.RTV_ERR_ARG
+    assert lib.rtv_shared_attention_workspace(None, C.byref(q), C.byref(kv), None, C.byref(n)) == L.RTV_ERR_ARG
+    assert n.value == 7
+    lib.rtv_ops_destroy(None)
+    assert lib.rtv_ops_last_error(None) == b"null operator handle"
+
+
+def test_cache_operators_refuse_host_tensors_and_types_before_the_library():
+    import torch
+    from flow_matching_action_dm0_b200 import CacheOps
+    ops = object.__new__(CacheOps)      # no GPU here: the checks come before the handle is used
+    ops.device, ops.h, ops._torch_device = 0, None, torch.device("cuda", 0)
+    x = torch.zeros((1, 2, 1, 64))
+    with pytest.raises(ValueError):
+        ops.write(None, x, x)
+    with pytest.raises(ValueError):
+        ops.cross_attention(x, (x, x))
+    with pytest.raises(ValueError):
+        ops.cross_attention(x[0], (x, x))
+    with pytest.raises(ValueError):
+        ops.shared_attention(x, (x[0], x[0]), own_lens=x)
