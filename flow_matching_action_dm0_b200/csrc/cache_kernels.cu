@@ -160,29 +160,16 @@ __host__ __device__ constexpr int attn_f32_smem(int bm, int d) {
   return 4 * (bm * (d + 4) + kKeys * (d + 4) + kKeys * d + bm * (kKeys + 4) + kKeys);
 }
 
-template <typename QT>
-__device__ __forceinline__ float4 load4(const QT* p) {
-  if (sizeof(QT) == 4) return *reinterpret_cast<const float4*>(p);
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xFFFF0000u));
-}
-template <typename QT>
-__device__ __forceinline__ void store4(QT* p, float4 v) {
-  if (sizeof(QT) == 4) *reinterpret_cast<float4*>(p) = v;
-  else *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
-}
-// Four elements of a key or value row: QT values, or E4M3 codes times the row's scale.
-template <typename QT>
+// Four elements of a key or value row: fp32, or E4M3 codes times the row's scale.
 __device__ __forceinline__ float4 load_kv4(const void* base, const float* scales, bool f8, long long off, long long foff) {
-  if (!f8) return load4(reinterpret_cast<const QT*>(base) + off);
+  if (!f8) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
   const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) + off);
   const float s = scales[foff];
   const float2 a = e4m3x2_to_f32x2(w & 0xFFFFu), b = e4m3x2_to_f32x2(w >> 16);
   return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
-template <typename QT, int D, int BM>
+template <int D, int BM>
 __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ AttnCall c) {
   constexpr int TM = BM / 16, LD = D + 4, LP = kKeys + 4, C4 = D / 4;
   extern __shared__ __align__(16) float sm[];
@@ -201,7 +188,8 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
       const long long row = u.row0 + r;
       const long long b = row / c.plan.rows_b;
       const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, g = rr - t * c.group;
-      v = load4(reinterpret_cast<const QT*>(c.q) + b * c.qb + t * c.qt + (long long)(u.kvh * c.group + g) * c.qh + d);
+      v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(c.q) + b * c.qb + t * c.qt +
+                                           (long long)(u.kvh * c.group + g) * c.qh + d);
     }
     *reinterpret_cast<float4*>(Qs + r * LD + d) = v;
   }
@@ -232,8 +220,8 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
       if (Ok[r] != 0.f) {
         const long long off = bb * s.sb + (long long)(k0 + r) * s.st + u.kvh * s.sh + d;
         const long long foff = bb * s.fb + (long long)(k0 + r) * s.ft + u.kvh * s.fh;
-        kv = load_kv4<QT>(s.k, s.ks, f8, off, foff);
-        vv = load_kv4<QT>(s.v, s.vs, f8, off, foff);
+        kv = load_kv4(s.k, s.ks, f8, off, foff);
+        vv = load_kv4(s.v, s.vs, f8, off, foff);
       }
       *reinterpret_cast<float4*>(Ks + r * LD + d) = kv;
       *reinterpret_cast<float4*>(Vs + r * D + d) = vv;
@@ -332,10 +320,11 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
     const long long b = row / c.plan.rows_b;
     const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, h = u.kvh * c.group + rr - t * c.group;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-    QT* dst = reinterpret_cast<QT*>(c.out) + b * c.ob + t * c.ot + h * c.oh + 4 * tx;
+    float* dst = reinterpret_cast<float*>(c.out) + b * c.ob + t * c.ot + h * c.oh + 4 * tx;
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)
-      store4(dst + 64 * k, make_float4(acc[i][k].x * inv, acc[i][k].y * inv, acc[i][k].z * inv, acc[i][k].w * inv));
+      *reinterpret_cast<float4*>(dst + 64 * k) =
+          make_float4(acc[i][k].x * inv, acc[i][k].y * inv, acc[i][k].z * inv, acc[i][k].w * inv);
     if (c.lse && tx == 0)
       c.lse[(b * c.Tq + t) * c.Hq + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
   }
@@ -402,10 +391,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     c.lse[(b * c.Tq + t) * c.Hq + h] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <typename QT, int D, int BM>
+template <int D, int BM>
 cudaError_t launch_f32(const AttnCall& c, cudaStream_t st) {
   const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + (long long)c.B * c.plan.tiles_e * c.plan.ne), c.Hkv);
-  attn_f32_kernel<QT, D, BM><<<grid, 256, attn_f32_smem(BM, D), st>>>(c);
+  attn_f32_kernel<D, BM><<<grid, 256, attn_f32_smem(BM, D), st>>>(c);
   return cudaGetLastError();
 }
 
@@ -423,16 +412,16 @@ cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, combine_kernel<QT, D>, c);
 }
 
-template <typename QT, int D>
+template <int D>
 cudaError_t launch_all(const AttnCall& c, cudaStream_t st) {
-  cudaError_t e = c.plan.bm == 16 ? launch_f32<QT, D, 16>(c, st) : launch_f32<QT, D, 64>(c, st);
-  if (e == cudaSuccess && c.plan.n_slots > 1) e = launch_combine<QT, D>(c, st);
-  return e;
+  cudaError_t e = c.bf16 ? launch_attention_tc(c, st) : c.plan.bm == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
+  if (e != cudaSuccess || c.plan.n_slots == 1) return e;
+  return c.bf16 ? launch_combine<__nv_bfloat16, D>(c, st) : launch_combine<float, D>(c, st);
 }
 
-template <typename QT, int D, int BM>
+template <int D, int BM>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(attn_f32_kernel<QT, D, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attn_f32_kernel<D, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               attn_f32_smem(BM, D));
 }
 
@@ -472,16 +461,17 @@ cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
 AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   AttnPlan p{};
   p.rows_b = c.Tq * c.group;
-  p.kt = kKeys;
-  p.bm = p.rows_b <= 16 ? 16 : 64;
+  p.kt = c.bf16 ? 128 : kKeys;
+  p.bm = c.bf16 ? 128 : p.rows_b <= 16 ? 16 : 64;
+  const bool f8 = (c.pre.len > 0 && c.pre_f8) || (c.own.len > 0 && c.own_f8);
+  const int slots = num_sms * (c.bf16 ? attention_tc_ctas_per_sm(c.D, f8) : 2);   // CTAs that run at once
   const int tb = (p.rows_b + p.bm - 1) / p.bm;
   // Rows of several elements share a tile (and its pass over the prefix) when
-  // one element's rows would leave most of it empty.
+  // one element's rows would leave half of it empty.
   const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= p.bm / 2;
   auto split = [&](long long units, int keys) {
     const int tiles = (keys + p.kt - 1) / p.kt;
-    const long long want = units * c.Hkv >= 2 * num_sms ? 1 : (2LL * num_sms) / (units * c.Hkv);
-    return (int)std::max(1LL, std::min<long long>({want, tiles, 64}));
+    return (int)std::max(1LL, std::min<long long>({slots / (units * c.Hkv), tiles, 64}));
   };
   if (stack) {
     p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm - 1) / p.bm);
@@ -504,30 +494,20 @@ size_t attention_workspace(const AttnCall& c) {
 cudaError_t configure_attention() {
   cudaError_t e = cudaSuccess;
   auto chain = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-  chain(set_smem<float, 64, 16>());
-  chain(set_smem<float, 64, 64>());
-  chain(set_smem<float, 128, 16>());
-  chain(set_smem<float, 128, 64>());
-  chain(set_smem<float, 256, 16>());
-  chain(set_smem<float, 256, 64>());
-  chain(set_smem<__nv_bfloat16, 64, 16>());
-  chain(set_smem<__nv_bfloat16, 64, 64>());
-  chain(set_smem<__nv_bfloat16, 128, 16>());
-  chain(set_smem<__nv_bfloat16, 128, 64>());
-  chain(set_smem<__nv_bfloat16, 256, 16>());
-  chain(set_smem<__nv_bfloat16, 256, 64>());
+  chain(set_smem<64, 16>());
+  chain(set_smem<64, 64>());
+  chain(set_smem<128, 16>());
+  chain(set_smem<128, 64>());
+  chain(set_smem<256, 16>());
+  chain(set_smem<256, 64>());
+  chain(configure_attention_tc());
   return e;
 }
 
-cudaError_t launch_attention(AttnCall& c, void* workspace, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st) {
   c.part_o = (float*)workspace;
   c.part_ml = c.part_o + (size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * c.D;
-  if (c.bf16)
-    return c.D == 64    ? launch_all<__nv_bfloat16, 64>(c, st)
-           : c.D == 128 ? launch_all<__nv_bfloat16, 128>(c, st)
-                        : launch_all<__nv_bfloat16, 256>(c, st);
-  return c.D == 64 ? launch_all<float, 64>(c, st) : c.D == 128 ? launch_all<float, 128>(c, st) : launch_all<float, 256>(c, st);
+  return c.D == 64 ? launch_all<64>(c, st) : c.D == 128 ? launch_all<128>(c, st) : launch_all<256>(c, st);
 }
 
 }  // namespace rtv

@@ -162,7 +162,8 @@ rtv_status attention_shape(rtv_ops* h, const rtv_queries* q, const rtv_kv* pre, 
   if (q->dtype != RTV_F32 && q->dtype != RTV_BF16) return ofail(h, RTV_ERR_ARG, "queries: fp32 or bf16 expected");
   if (q->batch < 0 || q->n_tokens < 0 || q->n_heads <= 0) return ofail(h, RTV_ERR_SHAPE, "queries: bad sizes");
   OTRY(check_dim(h, q->head_dim));
-  if (!std::isfinite(q->scale)) return ofail(h, RTV_ERR_ARG, "queries: scale is not finite");
+  if (!std::isfinite(q->scale) || !std::isnormal(q->scale * 1.4426950408889634f))
+    return ofail(h, RTV_ERR_ARG, "queries: scale must be a normal number");
   const rtv_kv* any = own ? own : pre;
   for (const rtv_kv* a : {pre, own}) {
     if (!a) continue;
@@ -248,7 +249,7 @@ rtv_status attention(rtv_ops* h, const rtv_queries* q, const rtv_kv* pre, const 
   c.status = h->status;
   c.timeout_ns = kTimeoutNs;
   DeviceGuard dg(h->device);
-  return launched(h, launch_attention(c, workspace, h->num_sms, (cudaStream_t)stream), "attention");
+  return launched(h, launch_attention(c, workspace, (cudaStream_t)stream), "attention");
 }
 
 }  // namespace

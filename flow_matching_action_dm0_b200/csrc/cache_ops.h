@@ -64,9 +64,13 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms);
 // Bytes of the partial results of a planned call.
 size_t attention_workspace(const AttnCall& c);
 // Enqueues a planned call; workspace as above.
-cudaError_t launch_attention(AttnCall& c, void* workspace, int num_sms, cudaStream_t st);
+cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st);
 // Sets the kernels' attributes on the current device (outside any capture).
 cudaError_t configure_attention();
+// The tensor-core kernel (bf16 queries).
+cudaError_t configure_attention_tc();
+cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st);
+int attention_tc_ctas_per_sm(int D, bool f8);
 
 // One tensor of rows [outer][batch][token][head][D] for the cache kernels;
 // strides in elements, the outer index (keys, values, or layers of both)

@@ -438,7 +438,7 @@ typedef struct {
  * Queries and where their attention goes: q and out [batch][n_tokens]
  * [n_heads][head_dim] in dtype (RTV_F32 or RTV_BF16); lse, when not NULL, is
  * dense [batch][n_tokens][n_heads] fp32: the natural logarithm of the sum of
- * exp(score).  score = scale * q.k.  n_heads is a multiple of the keys'
+ * exp(score).  score = scale * q.k, scale finite and not 0.  n_heads is a multiple of the keys'
  * heads; query head h reads key/value head h / (n_heads / kv heads).  A query
  * that sees no key gives out = 0 and lse = -infinity.
  */
