@@ -2,10 +2,10 @@
 // cross attention, for a prefix shared by a batch and for each element's own
 // keys, bf16 or E4M3.
 //
-// A CTA takes 128 rows (query token x head of a KV head's group) against a
-// range of 128-key tiles, in one pass:
-//   S = Q K^T    tcgen05, 128 x 128, K chunks of 64 dims from a ring of 16 KB
-//                stages filled by TMA                             -> TMEM
+// A CTA takes up to 256 rows (query token x head of a KV head's group; 128 at
+// head_dim 256) against a range of 128-key tiles, in one pass over them:
+//   S = Q K^T    tcgen05, 128 x 128, K in chunks of 64 dims from a ring of
+//                16 KB stages filled by TMA                        -> TMEM
 //   P = 2^(S - m) a thread per row, straight from TMEM; the row's sum is kept
 //                in fp32, P rounded to bf16 (the MMA's input type) and
 //                written over S in TMEM
@@ -13,9 +13,16 @@
 //                dims) as an MN-major operand, so V is never transposed
 // m is the running maximum, raised (and O rescaled) only when a row's maximum
 // has grown by more than 8 in base 2: weights stay below 2^8, and the result
-// is the same quotient.  Roles: warp 0 issues the loads, warp 1 the MMAs,
-// warps 4-7 the softmax (and the output); with an E4M3 source warps 8-11 widen
-// codes to bf16 stages (exactly), and the scales multiply S and P in fp32.
+// is the same quotient.
+//
+// Work goes in steps q that alternate between two S buffers and two softmax
+// groups of four warps: with more than 128 rows, step q is row tile q & 1
+// against key tile q >> 1 (both row tiles read a key tile's stages once);
+// with fewer, key tile q for the one row tile, the groups handing its maximum
+// on.  The MMA warp issues S(q + 1) before PV(q), so that the tensor cores
+// have work while a group exponentiates.  Warp 0 issues the loads, warp 1 the
+// MMAs; with an E4M3 source six warps widen codes to bf16 stages (exactly),
+// and the scales multiply S and P in fp32.
 #include <cuda.h>
 
 #include <algorithm>
@@ -45,16 +52,21 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int NC = D / 64;                       // stages of a K or V tile
   static constexpr int VK = 8192 / D;                     // keys of a V stage
-  static constexpr bool kTwo = D <= 128 && !F8;           // two CTAs share an SM
-  static constexpr int TCOLS = kTwo ? 256 : 512;          // tensor memory columns of the CTA
-  static constexpr int NSB = kTwo ? 1 : 2;                // S buffers
-  static constexpr int QB = kTile * D * 2;
-  static constexpr int NST = kTwo ? (D == 64 ? 5 : 4) : F8 ? 6 : 10;
-  static constexpr int NRAW = F8 ? 6 : 0;
-  static constexpr int kThreads = F8 ? 384 : 256;
-  static constexpr bool kHold = !F8 && !kTwo;             // a thread has the registers for a row of S
-  static constexpr int kOff = QB + NST * kStage + NRAW * kRaw;   // barriers behind the tiles
-  static constexpr int kSmem = 1024 + kOff + 512 + (F8 ? 2 * 2 * kTile * 4 : 0);
+  static constexpr int MT = D == 256 ? 1 : 2;             // row tiles that fit the tensor memory
+  static constexpr int QB = kTile * D * 2;                // bytes of a Q tile
+  static constexpr int NST = F8 ? 6 : 10;
+  static constexpr int kThreads = F8 ? 512 : 384;
+  static constexpr int kSoft = 4;                         // first softmax warp
+  // Registers of a softmax thread (it holds a row of S) and of the others:
+  // 8 warps of the one and 4 (8) of the other use what the CTA was launched with.
+  static constexpr int kLaunchRegs = F8 ? 128 : 168, kSoftRegs = F8 ? 168 : 208, kOtherRegs = 88;
+  static_assert(256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "register shares");
+  static constexpr int kOff = MT * QB + NST * kStage + (F8 ? NST * kRaw : 0);   // barriers behind the tiles
+  static constexpr int kSmall = 512 + 512 + 4 * 128 + (F8 ? 4 * 2 * kTile * 4 : 0);   // barriers, exchange, scales
+  static constexpr int kSmem = 1024 + kOff + kSmall;
+  static constexpr int kRowBytes = D * 4 + 16;            // a staged output row
+  static_assert(MT * kTile * kRowBytes <= kOff, "output rows are staged where the tiles were");
+  static_assert(kSmem <= 232448 - 64, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int t, int h, int b, uint64_t* bar) {
@@ -105,12 +117,13 @@ __device__ __forceinline__ void tmem_ld_32_async(uint32_t taddr, uint32_t (&r)[3
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : W8(0), W8(8), W8(16), W8(24)::"memory");
 }
-__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16_raw(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      I8(0), I8(8), I8(16), I8(24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R8(0), R8(8)
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -140,22 +153,21 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
   return ptx::pack_bf16x2(f.x, f.y);
 }
 
-// What every role derives from the unit: the order of the tiles' loads, which
-// is that of the MMAs: with two S buffers K(0), K(1), V(0), K(2), V(1), ...,
-// with one K(0), V(0), K(1), V(1), ...
-template <int NSB>
+// The order of a unit's loads is that of their first use: with two row tiles
+// K(0), V(0), K(1), V(1), ...; with one, S runs a key tile ahead:
+// K(0), K(1), V(0), K(2), V(1), ...
 struct Order {
-  int n;                                          // tiles
-  __device__ int count() const { return 2 * n; }
-  // i-th load: tile * 2 + (1: values)
+  int n;                                          // key tiles
+  bool two;                                       // row tiles: two, or one
+  // i-th load: key tile * 2 + (1: values)
   __device__ int at(int i) const {
-    if (NSB == 1) return i;
+    if (two) return i;
     if (i == 0) return 0;
     if (i == 2 * n - 1) return 2 * (n - 1) + 1;
     return (i & 1) ? 2 * ((i + 1) >> 1) : 2 * ((i >> 1) - 1) + 1;
   }
-  // loads before V(j)
-  __device__ int before_v(int j) const { return NSB == 1 ? 2 * j + 1 : min(j + 2, n) + j; }
+  __device__ int of_k(int j) const { return two ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+  __device__ int of_v(int j) const { return two ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
 };
 
 struct TileAt {
@@ -175,162 +187,182 @@ __device__ __forceinline__ bool has_hidden(const AttnCall& c, const TileAt& t) {
   return t.nk < kTile || (t.pre ? c.pre.mask : c.own.mask) != nullptr;
 }
 
+// Named barriers: 1 all softmax warps, 2 and 3 a softmax group, 4.. a pair of warps of the groups.
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) from shared to global memory.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
 template <int D, bool F8>
-__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, Cfg<D, F8>::kTwo ? 2 : 1)
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     attn_cache_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnMaps maps) {
   using C = Cfg<D, F8>;
-  constexpr int NC = C::NC, NSB = C::NSB, NST = C::NST, VK = C::VK;
-  constexpr int NRAW = F8 ? C::NRAW : 1;
+  constexpr int NC = C::NC, NST = C::NST, VK = C::VK;
   extern __shared__ uint8_t sm_raw[];
   __shared__ int s_abort;
   uint8_t* Qs = (uint8_t*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* ring = Qs + C::QB;
-  uint8_t* raw = ring + NST * kStage;
-  uint64_t* bars = (uint64_t*)(Qs + C::kOff);
-  uint64_t* ready = bars;                         // [NST] stage holds its operand
-  uint64_t* empty = ready + NST;                  // [NST] its MMAs have completed
-  uint64_t* s_full = empty + NST;                 // [2] S of a buffer is complete
+  uint8_t* ring = Qs + C::MT * C::QB;
+  uint8_t* raw = ring + NST * kStage;             // E4M3: the codes of each stage
+  uint64_t* ready = (uint64_t*)(Qs + C::kOff);    // [NST] the stage holds its operand
+  uint64_t* empty = ready + NST;                  // [NST] the stage's MMAs have completed
+  uint64_t* raw_full = empty + NST;               // [NST] E4M3
+  uint64_t* raw_empty = raw_full + NST;           // [NST]
+  uint64_t* s_full = raw_empty + NST;             // [2] S of a buffer is complete
   uint64_t* p_ready = s_full + 2;                 // [2] P of a buffer is written (and hidden values are zeroed)
-  uint64_t* pv_done = p_ready + 2;                // O += P V has completed
-  uint64_t* q_ready = pv_done + 1;
-  uint64_t* o_done = q_ready + 1;                 // every MMA of the CTA has completed
-  uint64_t* v_landed = o_done + 1;                // values of a tile with hidden keys are in their stages
-  uint64_t* raw_full = v_landed + 1;              // [NRAW]
-  uint64_t* raw_empty = raw_full + NRAW;          // [NRAW]
-  uint32_t* tslot = (uint32_t*)(raw_empty + NRAW);
-  uint32_t* seen = tslot + 2;                     // [2][4] visible keys of a tile, 32 to a word
-  float* scales = (float*)(bars + 64);            // [2][K, V][128] of a tile (E4M3)
-  static_assert((2 * NST + 8 + 2 * NRAW) * 8 + 8 + 32 <= 512, "barriers fit their space");
+  uint64_t* v_landed = p_ready + 2;               // [2] the values of a step with hidden keys are in their stages
+  uint64_t* q_ready = v_landed + 2;               // [2] Q rows of a group
+  uint64_t* pv_done = q_ready + 2;                // one row tile: O += P V of a step has completed
+  uint64_t* o_done = pv_done + 1;                 // every MMA of the CTA has completed
+  uint32_t* tslot = (uint32_t*)(o_done + 1);
+  static_assert((4 * NST + 10) * 8 + 8 <= 512, "barriers fit their space");
+  float* m_row = (float*)(Qs + C::kOff + 512);    // [128] the maximum that the groups hand on (one row tile)
+  uint32_t* seen = (uint32_t*)(m_row + 128);      // [2 groups][4] visible keys of the group's tile
+  float* scales = m_row + 256;                    // E4M3: [2 groups][2][K, V][128]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const AttnUnit u = attn_unit(c);
-  const int n = u.t1 - u.t0;
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < NST; ++i) {
       ptx::mbar_init(&ready[i], 1);
       ptx::mbar_init(&empty[i], 1);
+      if (F8) {
+        ptx::mbar_init(&raw_full[i], 1);
+        ptx::mbar_init(&raw_empty[i], 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s_full[i], 1);
       ptx::mbar_init(&p_ready[i], 128);
+      ptx::mbar_init(&v_landed[i], 1);
+      ptx::mbar_init(&q_ready[i], 128);
     }
     ptx::mbar_init(pv_done, 1);
-    ptx::mbar_init(q_ready, C::kThreads - 64);
     ptx::mbar_init(o_done, 1);
-    ptx::mbar_init(v_landed, 1);
-    if (F8)
-      for (int i = 0; i < NRAW; ++i) {
-        ptx::mbar_init(&raw_full[i], 1);
-        ptx::mbar_init(&raw_empty[i], 1);
-      }
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tslot, C::TCOLS);
+    ptx::tmem_alloc(tslot, 512);
     ptx::tmem_relinquish();
   }
+  const AttnUnit u = attn_unit(c);
+  const int n = u.t1 - u.t0;
+  const bool two = C::MT == 2 && u.nrows > kTile;
+  const int steps = two ? 2 * n : n;
+  const Order order{n, two};
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tslot;
-  const uint32_t o_tmem = tmem + NSB * kTile;     // S buffers first, then O
-  const long long limit = c.timeout_ns;
-  const Order<NSB> order{n};
+  const uint32_t o_tmem = tmem + 2 * kTile;       // two S buffers, then O of each row tile
   // After a wait has run out every other one gives up at once, so that all
   // warps reach the end (and the barriers among them) without their data.
   auto wait = [&](uint64_t* bar, int parity) {
-    if (*(volatile int*)&s_abort) return false;
-    if (ptx::mbar_wait(bar, (uint32_t)parity & 1u, limit)) return true;
-    atomicOr(c.status, RTV_DEV_TIMEOUT);
-    atomicOr(&s_abort, 1);
+    const uint32_t par = (uint32_t)parity & 1u;
+    if (ptx::mbar_try_wait(bar, par)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!*(volatile int*)&s_abort) {
+      if (ptx::mbar_try_wait(bar, par)) return true;
+      if ((long long)(ptx::globaltimer() - t0) > c.timeout_ns) {
+        atomicOr(c.status, RTV_DEV_TIMEOUT);
+        atomicOr(&s_abort, 1);
+      }
+    }
     return false;
   };
+  // One load of the order: the boxes of a stage, K chunk or V keys.
+  auto load = [&](int o, int cc, uint8_t* dst, uint64_t* bar, int row) {
+    const TileAt t = tile_at(u, u.t0 + (o >> 1));
+    const CUtensorMap* map = t.pre ? ((o & 1) ? &maps.pre_v : &maps.pre_k) : ((o & 1) ? &maps.own_v : &maps.own_k);
+    const int h = u.kvh * (t.pre ? maps.pre_h : maps.own_h), b = t.pre ? 0 : u.b * maps.own_b;
+    ptx::mbar_expect_tx(bar, 128u * row);
+    if (!(o & 1)) {
+      tma_load_4d(dst, map, 64 * cc, t.k0, h, b, bar);
+    } else {
+#pragma unroll
+      for (int dc = 0; dc < NC; ++dc) tma_load_4d(dst + dc * VK * row, map, 64 * dc, t.k0 + cc * VK, h, b, bar);
+    }
+  };
+  auto is_codes = [&](int o) { return F8 && (tile_at(u, u.t0 + (o >> 1)).pre ? c.pre_f8 : c.own_f8); };
 
   if (warp == 0) {
-    // ---- loads -------------------------------------------------------------
+    // ---- loads: bf16 into the stages, or codes into the stages' raw slots ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
-      int st = 0, rw = 0;                         // stages and raw stages filled so far
+      int st = 0;
+      uint32_t used = 0;                          // parity of each raw slot's uses
       bool ok = true;
-      for (int i = 0; i < order.count() && ok; ++i) {
+      for (int i = 0; i < 2 * n && ok; ++i) {
         const int o = order.at(i);
-        const bool val = o & 1;
-        const TileAt t = tile_at(u, u.t0 + (o >> 1));
-        const CUtensorMap* map = t.pre ? (val ? &maps.pre_v : &maps.pre_k) : (val ? &maps.own_v : &maps.own_k);
-        const int h = t.pre ? u.kvh * maps.pre_h : u.kvh * maps.own_h, b = t.pre ? 0 : u.b * maps.own_b;
-        const bool codes = F8 && (t.pre ? c.pre_f8 : c.own_f8);
+        const bool codes = is_codes(o);
         for (int cc = 0; cc < NC && ok; ++cc, ++st) {
-          uint8_t* dst;
-          uint64_t* bar;
-          int row;                                // bytes of a row
-          if (codes) {
-            const int r = rw % NRAW;
-            if (!(ok = wait(&raw_empty[r], rw / NRAW + 1))) break;
-            dst = raw + r * kRaw;
-            bar = &raw_full[r];
-            row = 64;
-            ++rw;
+          const int s = st % NST;
+          if (F8) {
+            if (!codes) continue;                 // its stage's warp loads it
+            if (!(ok = wait(&raw_empty[s], (int)(used >> s) + 1))) break;
+            used ^= 1u << s;
+            load(o, cc, raw + s * kRaw, &raw_full[s], 64);
           } else {
-            // (behind codes: the converters wait for these stages in their own
-            // time, and a parity tells a phase only from its neighbours)
-            if (F8 && rw > 0 && !(ok = wait(&raw_empty[(rw - 1) % NRAW], (rw - 1) / NRAW))) break;
-            const int s = st % NST;
             if (!(ok = wait(&empty[s], st / NST + 1))) break;
-            dst = ring + s * kStage;
-            bar = &ready[s];
-            row = 128;
+            load(o, cc, ring + s * kStage, &ready[s], 128);
           }
-          ptx::mbar_expect_tx(bar, 128u * row);
-          if (!val) tma_load_4d(dst, map, 64 * cc, t.k0, h, b, bar);
-          else
-#pragma unroll
-            for (int dc = 0; dc < NC; ++dc) tma_load_4d(dst + dc * VK * row, map, 64 * dc, t.k0 + cc * VK, h, b, bar);
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMAs --------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0 && n > 0) {
       const uint32_t id_s = ptx::idesc_bf16_f32(128, kTile), id_o = ptx::idesc_bf16_f32(128, D) | kBTransposed;
-      const uint32_t qa = ptx::smem_u32(Qs), ra = ptx::smem_u32(ring);
-      int st = 0;
-      bool ok = wait(q_ready, 0);
-      for (int i = 0; i < order.count() && ok; ++i) {
-        const int o = order.at(i), j = o >> 1, buf = NSB == 1 ? 0 : j & 1;
+      const uint64_t qd = ptx::sw128_kmajor_desc(ptx::smem_u32(Qs)), kd = ptx::sw128_kmajor_desc(ptx::smem_u32(ring));
+      const uint64_t vd = sw128_mnmajor_desc(ptx::smem_u32(ring), VK * 128);
+      bool ok = wait(&q_ready[0], 0);
+      if (!two) ok = wait(&q_ready[1], 0) && ok;
+      for (int i = 0; i < 2 * steps && ok; ++i) {
+        // S(0), S(1), PV(0), S(2), PV(1), ..., PV(steps - 1)
+        const bool pv = i == 2 * steps - 1 || (i > 0 && !(i & 1));
+        const int q = pv ? (i == 2 * steps - 1 ? steps - 1 : (i >> 1) - 1) : (i + 1) >> 1;
+        const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
+        const bool last_use = !two || rt == 1;    // of the key tile's stages
         const uint32_t s_tmem = tmem + buf * kTile;
-        if (!(o & 1)) {
-          // S(j) overwrites P(j - NSB)
-          if (j >= NSB && !(ok = wait(pv_done, j - NSB))) break;
+        if (!pv) {
+          // (S(q) is written over P(q - 2), whose MMA comes before it in this thread's order)
+          if (q == 1 && two && !(ok = wait(&q_ready[1], 0))) break;
+          int st = order.of_k(j) * NC;
           for (int cc = 0; cc < NC && ok; ++cc, ++st) {
             const int s = st % NST;
             if (!(ok = wait(&ready[s], st / NST))) break;
             ptx::tc_fence_after();
+            const uint64_t qa = qd + (uint64_t)((rt * C::QB + cc * 16384) >> 4), ka = kd + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::umma_bf16(s_tmem, ptx::sw128_kmajor_desc(qa + cc * 16384 + kk * 32),
-                             ptx::sw128_kmajor_desc(ra + s * kStage + kk * 32), id_s, (cc | kk) != 0);
-            ptx::umma_commit(&empty[s]);
+            for (int kk = 0; kk < 4; ++kk) ptx::umma_bf16(s_tmem, qa + 2 * kk, ka + 2 * kk, id_s, (cc | kk) != 0);
+            if (last_use) ptx::umma_commit(&empty[s]);
           }
           if (ok) ptx::umma_commit(&s_full[buf]);
         } else {
-          if (has_hidden(c, tile_at(u, u.t0 + j))) {
+          int st = order.of_v(j) * NC;
+          if (rt == 0 && has_hidden(c, tile_at(u, u.t0 + j))) {
             for (int cc = 0; cc < NC && ok; ++cc) ok = wait(&ready[(st + cc) % NST], (st + cc) / NST);
             if (!ok) break;
-            ptx::mbar_arrive(v_landed);
+            ptx::mbar_arrive(&v_landed[buf]);
           }
-          if (!(ok = wait(&p_ready[buf], j / NSB))) break;
+          if (!(ok = wait(&p_ready[buf], q >> 1))) break;
           for (int cc = 0; cc < NC && ok; ++cc, ++st) {
             const int s = st % NST;
             if (!(ok = wait(&ready[s], st / NST))) break;
             ptx::tc_fence_after();
+            const uint64_t va = vd + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
             for (int kk = 0; kk < VK / 16; ++kk)
-              umma_bf16_ts(o_tmem, s_tmem + (cc * VK + kk * 16) / 2,
-                           sw128_mnmajor_desc(ra + s * kStage + kk * 2048, VK * 128), id_o, (j | cc | kk) != 0);
-            ptx::umma_commit(&empty[s]);
+              umma_bf16_ts(o_tmem + rt * kTile, s_tmem + (cc * VK + kk * 16) / 2, va + kk * (2048 >> 4), id_o,
+                           (j | cc | kk) != 0);
+            if (last_use) ptx::umma_commit(&empty[s]);
           }
-          if (ok) ptx::umma_commit(pv_done);
+          if (ok && !two) ptx::umma_commit(pv_done);
         }
       }
       // every MMA completes before the tensor memory is read for the last time and freed
@@ -338,265 +370,301 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, Cfg<D, F8>::kTwo ? 2 : 1
       if (!ptx::mbar_wait(o_done, 0, kDrainNs)) atomicOr(c.status, RTV_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else {
-    // ---- Q rows, 16 bytes a lane, in the K-major swizzled layout ------------
-    {
-      constexpr int CPR = D / 8;                  // 16-byte chunks of a row
-      const uint32_t flip = c.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale becomes -q and its magnitude
-      for (int i = tid - 64; i < kTile * CPR; i += C::kThreads - 64) {
-        const int r = i / CPR, ch = i - r * CPR;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < u.nrows) {
-          const long long row = u.row0 + r;
-          const int b = (int)(row / c.plan.rows_b), rr = (int)(row - (long long)b * c.plan.rows_b);
-          const int t = rr / c.group, g = rr - t * c.group;
-          v = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + b * c.qb + t * c.qt +
-                                              (long long)(u.kvh * c.group + g) * c.qh + ch * 8);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+  } else if (warp < C::kSoft || warp >= C::kSoft + 8) {
+    // ---- E4M3 codes to bf16 stages: a warp per stage of the ring -------------
+    // (every use of a stage is its warp's, so the phases it waits for follow
+    // one another: a parity tells a phase only from its neighbours)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (F8) {
+      const int s = warp < 4 ? warp - 2 : warp - 10;   // warps 2, 3, 12..15
+      uint8_t* dst = ring + s * kStage;
+      const uint8_t* src = raw + s * kRaw + lane * 16;
+      uint32_t used = 0;
+      int use = 0;                                // uses of the stage so far
+      for (int i = 0; i < 2 * n * NC; ++i) {
+        if (i % NST != s) continue;
+        const int o = order.at(i / NC), cc = i % NC;
+        if (!is_codes(o)) {
+          if (wait(&empty[s], use + 1) && lane == 0) load(o, cc, dst, &ready[s], 128);
+          __syncwarp();
+          ++use;
+          continue;
         }
-        *reinterpret_cast<uint4*>(Qs + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        wait(&raw_full[s], used);
+        used ^= 1u;
+        wait(&empty[s], use + 1);
+        ++use;
+        const int c16 = lane & 3;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (h * 8 + k) * 512);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = (h * 8 + k) * 8 + (lane >> 2);
+            uint4 a, b;
+            a.x = e4m3x2_to_bf16x2(v[k].x & 0xFFFFu), a.y = e4m3x2_to_bf16x2(v[k].x >> 16);
+            a.z = e4m3x2_to_bf16x2(v[k].y & 0xFFFFu), a.w = e4m3x2_to_bf16x2(v[k].y >> 16);
+            b.x = e4m3x2_to_bf16x2(v[k].z & 0xFFFFu), b.y = e4m3x2_to_bf16x2(v[k].z >> 16);
+            b.z = e4m3x2_to_bf16x2(v[k].w & 0xFFFFu), b.w = e4m3x2_to_bf16x2(v[k].w >> 16);
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((2 * c16) ^ (row & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((2 * c16 + 1) ^ (row & 7)) << 4)) = b;
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&ready[s]);
+          ptx::mbar_arrive(&raw_empty[s]);
+        }
+      }
+    }
+  } else {
+    // ---- softmax: a row a thread ----------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    const int grp = (warp - C::kSoft) >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane;            // row of the row tile, and key whose visibility this thread looks up
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int tile_row = two ? grp * kTile : 0;
+    const bool live = tile_row + 32 * quarter < u.nrows;   // the warp has rows
+    const bool mine = tile_row + r < u.nrows;
+    const long long row = u.row0 + (mine ? tile_row + r : 0);
+    const unsigned b = (unsigned)row / (unsigned)c.plan.rows_b, rr = (unsigned)row - b * (unsigned)c.plan.rows_b;
+    const unsigned t_row = rr / (unsigned)c.group, h_row = u.kvh * c.group + rr - t_row * (unsigned)c.group;
+    // Q rows: the warp's own 32 (with one row tile the groups take 16 each), 16 bytes a lane
+    {
+      constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows of a warp's step
+      const long long off = b * c.qb + (long long)t_row * c.qt + (long long)h_row * c.qh;
+      const uint32_t flip = c.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale becomes -q and its magnitude
+      uint8_t* qt = Qs + (two ? grp * C::QB : 0);
+      const int r0 = two ? 0 : 16 * grp, nr = two ? 32 : 16, ch = lane % CPR;
+#pragma unroll 1
+      for (int i = 0; i < nr; i += 8 * RPI) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rl = r0 + i + k * RPI + lane / CPR;           // row of the warp's 32
+          const long long o = __shfl_sync(0xffffffffu, off, rl & 31);
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (i + k * RPI < nr && tile_row + 32 * quarter + rl < u.nrows)
+            v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + o + ch * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rq = 32 * quarter + r0 + i + k * RPI + lane / CPR;
+          if (i + k * RPI >= nr) break;
+          v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+          *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4)) = v[k];
+        }
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(q_ready);
+      ptx::mbar_arrive(&q_ready[grp]);
     }
-    if (warp >= 8) {
-      // ---- E4M3 codes to bf16 stages ---------------------------------------
-      if (F8) {
-        const int ct = tid - 256;
-        int st = 0, rw = 0;
-        for (int i = 0; i < order.count(); ++i) {
-          const TileAt t = tile_at(u, u.t0 + (order.at(i) >> 1));
-          if (!(t.pre ? c.pre_f8 : c.own_f8)) {
-            st += NC;
-            continue;
-          }
-          for (int cc = 0; cc < NC; ++cc, ++st, ++rw) {
-            const int s = st % NST, r = rw % NRAW;
-            wait(&raw_full[r], rw / NRAW);
-            wait(&empty[s], st / NST + 1);
-            const uint8_t* src = raw + r * kRaw;
-            uint8_t* dst = ring + s * kStage;
-            uint4 v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (q * 128 + ct) * 16);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int id = q * 128 + ct, row = id >> 2, c16 = id & 3;
-              const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint4 o;
-                o.x = e4m3x2_to_bf16x2(w[2 * h] & 0xFFFFu);
-                o.y = e4m3x2_to_bf16x2(w[2 * h] >> 16);
-                o.z = e4m3x2_to_bf16x2(w[2 * h + 1] & 0xFFFFu);
-                o.w = e4m3x2_to_bf16x2(w[2 * h + 1] >> 16);
-                *reinterpret_cast<uint4*>(dst + row * 128 + (((2 * c16 + h) ^ (row & 7)) << 4)) = o;
-              }
-            }
-            ptx::fence_proxy_async_smem();
-            named_sync(2, 128);
-            if (ct == 0) {
-              ptx::mbar_arrive(&ready[s]);
-              ptx::mbar_arrive(&raw_empty[r]);
-            }
-          }
-        }
-      }
-    } else if (warp >= 4) {
-      // ---- softmax: a row a thread --------------------------------------------
-      const int r = tid - 128;                    // row, and key whose visibility this thread looks up
-      const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
-      const float scale = fabsf(c.scale_log2);
-      const bool live = 32 * (warp - 4) < u.nrows;   // the warp has rows
-      float m = -INFINITY, l = 0.f;
-      int partial = 0;                            // tiles with hidden keys so far
-      // the scales of the next tile's key r are fetched a tile ahead
-      float ks = 0.f, vs = 0.f;
-      auto fetch = [&](int t) {
-        if (!F8 || t >= u.t1) return;
-        const TileAt a = tile_at(u, t);
-        ks = vs = 1.f;
-        if (!(a.pre ? c.pre_f8 : c.own_f8) || r >= a.nk) return;
-        const KvSource& s = a.pre ? c.pre : c.own;
-        const long long off = (a.pre ? 0 : u.b) * s.fb + (long long)(a.k0 + r) * s.ft + u.kvh * s.fh;
-        ks = s.ks[off];
-        vs = s.vs[off];
-      };
-      fetch(u.t0);
-      for (int j = 0; j < n; ++j) {
-        const int buf = NSB == 1 ? 0 : j & 1;
-        const TileAt t = tile_at(u, u.t0 + j);
-        const KvSource& src = t.pre ? c.pre : c.own;
-        const bool whole = !has_hidden(c, t);
-        if (!whole || F8) {
-          bool mine = true;
-          if (!whole) {
-            mine = r < t.nk && (!src.mask || src.mask[(t.pre ? 0 : u.b) * src.mask_sb + t.k0 + r]);
-            const uint32_t word = __ballot_sync(0xffffffffu, mine);
-            if (lane == 0) seen[(j & 1) * 4 + warp - 4] = word;
-          }
-          if (F8) {
-            scales[(j & 1) * 256 + r] = mine ? ks : 1.f;
-            scales[(j & 1) * 256 + 128 + r] = mine ? vs : 0.f;
-            fetch(u.t0 + j + 1);
-          }
-          named_sync(1, 128);
-        }
-        wait(&s_full[buf], j / NSB);
-        ptx::tc_fence_after();
-        const uint32_t s_tmem = tmem + buf * kTile + lanes;
-        const float* sc = scales + (j & 1) * 256;
-        if (!whole && live) {
-          // scores of hidden keys become -inf, so that nothing below looks at the mask
-#pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            const uint32_t vis = seen[(j & 1) * 4 + cc];
-            uint32_t y[32];
-            tmem_ld_32_async(s_tmem + 32 * cc, y);
-            tmem_wait_ld(y);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = (vis >> e) & 1u ? y[e] : 0xFF800000u;
-            tmem_st_32(s_tmem + 32 * cc, y);
-          }
-          tmem_wait_st();
-        }
-        if (live) {
-          // With registers to spare the whole row is held; otherwise it is read
-          // twice from tensor memory, 32 columns at a time.
-          float top = -INFINITY;
-          uint32_t x[C::kHold ? 4 : 1][32];
-          auto load = [&](int cc) {
-            tmem_ld_32_async(s_tmem + 32 * cc, x[C::kHold ? cc : 0]);
-            if (!C::kHold) tmem_wait_ld(x[0]);
-          };
-          if (C::kHold) {
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) load(cc);
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[C::kHold ? cc : 0]);
-          }
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            if (!C::kHold) load(cc);
-            uint32_t(&xc)[32] = x[C::kHold ? cc : 0];
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float y = __uint_as_float(xc[e]);
-              if (F8) y *= sc[32 * cc + e];
-              t4[e & 3] = fmaxf(t4[e & 3], y);
-            }
-            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
-          }
-          const float mn = fmaxf(m, top == -INFINITY ? -INFINITY : top * scale);
-          if (j == 0) {
-            m = mn;
-          } else if (__any_sync(0xffffffffu, mn - m > kLazy)) {
-            wait(pv_done, j - 1);
-            ptx::tc_fence_after();
-            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t y[32];
-              tmem_ld_32_async(o_tmem + lanes + 32 * cc, y);
-              tmem_wait_ld(y);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-              tmem_st_32(o_tmem + lanes + 32 * cc, y);
-            }
-            tmem_wait_st();
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            if (!C::kHold) load(cc);
-            uint32_t(&xc)[32] = x[C::kHold ? cc : 0];
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float y = __uint_as_float(xc[e + k]);
-                if (F8) y *= sc[32 * cc + e + k];
-                p[k] = ex2(fmaf(y, scale, -base));
-                l4[(e + k) & 3] += p[k];
-                if (F8) p[k] *= sc[128 + 32 * cc + e + k];
-              }
-              w[e / 2] = ptx::pack_bf16x2(p[0], p[1]);
-            }
-            tmem_st_16(s_tmem + 16 * cc, w);   // over S columns that have been read
-          }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          tmem_wait_st();
-        }
+    const float scale = fabsf(c.scale_log2);
+    float m = -INFINITY, l = 0.f;                 // l counts in units of 2^m
+    int partial = 0;                              // steps with hidden keys so far
+    // E4M3: the scales of key r of the group's next tile are fetched a step ahead
+    float ks = 1.f, vs = 1.f;
+    auto fetch = [&](int q) {
+      if (!F8 || q >= steps) return;
+      const TileAt a = tile_at(u, u.t0 + (two ? q >> 1 : q));
+      ks = vs = 1.f;
+      if (!(a.pre ? c.pre_f8 : c.own_f8) || r >= a.nk) return;
+      const long long fb = a.pre ? 0 : u.b * c.own.fb;
+      const long long off = fb + (long long)(a.k0 + r) * (a.pre ? c.pre.ft : c.own.ft) + u.kvh * (a.pre ? c.pre.fh : c.own.fh);
+      ks = (a.pre ? c.pre.ks : c.own.ks)[off];
+      vs = (a.pre ? c.pre.vs : c.own.vs)[off];
+    };
+    fetch(grp);
+    for (int q = grp; q < steps; q += 2) {
+      const int j = two ? q >> 1 : q;
+      const TileAt t = tile_at(u, u.t0 + j);
+      const bool whole = !has_hidden(c, t);
+      float* sc = scales + (grp * 2 + ((q >> 1) & 1)) * 256;
+      if (!whole || F8) {
+        bool vis = true;
         if (!whole) {
-          // hidden values become zeros: their weight is 0, and 0 times anything stored there must be 0
-          wait(v_landed, partial++);
-          if (!((seen[(j & 1) * 4 + warp - 4] >> lane) & 1u)) {
-            uint8_t* dst = ring + ((order.before_v(j) * NC + r / VK) % NST) * kStage + (r % VK) * 128;
-#pragma unroll 1
-            for (int q = 0; q < NC * 8; ++q)
-              *reinterpret_cast<uint4*>(dst + (q >> 3) * VK * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            ptx::fence_proxy_async_smem();
-          }
+          const uint8_t* mask = t.pre ? c.pre.mask : c.own.mask;
+          vis = r < t.nk && (!mask || mask[(t.pre ? 0 : u.b * c.own.mask_sb) + t.k0 + r]);
+          const uint32_t word = __ballot_sync(0xffffffffu, vis);
+          // (the group's last look at the words of its previous step was before its P was complete)
+          named_sync(2 + grp, 128);
+          if (lane == 0) seen[grp * 4 + quarter] = word;
         }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&p_ready[buf]);
+        if (F8) {
+          sc[r] = vis ? ks * scale : 1.f;         // the scale of the scores goes with the key's
+          sc[128 + r] = vis ? vs : 0.f;
+          fetch(q + 2);
+        }
+        named_sync(2 + grp, 128);
       }
-      // ---- output --------------------------------------------------------------
-      if (n > 0) wait(o_done, 0);
+      wait(&s_full[grp], q >> 1);
       ptx::tc_fence_after();
-      const bool split = c.plan.n_slots > 1;
-      const bool mine = r < u.nrows;
-      const long long row = u.row0 + (mine ? r : 0);
-      const int b = (int)(row / c.plan.rows_b), rr = (int)(row - (long long)b * c.plan.rows_b);
-      const int t = rr / c.group, h = u.kvh * c.group + rr - t * c.group;
-      const long long pr = part_row(c, u, row);
-      if (mine && split) {
-        // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
-        const float mo = l != l ? INFINITY : l == 0.f ? -INFINITY : m;
-        *reinterpret_cast<float2*>(c.part_ml + pr * 2) = make_float2(mo, l);
-      }
-      if (mine && !split && c.lse)
-        c.lse[((long long)b * c.Tq + t) * c.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const uint32_t s_tmem = tmem + grp * kTile + lanes;
       if (live) {
-        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(c.out) + b * c.ob + t * c.ot + h * c.oh;
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t x[32];
-          if (n > 0) {
-            tmem_ld_32_async(o_tmem + lanes + 32 * cc, x);
-            tmem_wait_ld(x);
-          } else {
+        uint32_t x[4][32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0u;
-          }
-          if (!mine) continue;
-          if (split) {
-            if (l == 0.f) continue;               // the join does not read an empty part
-            float4* dst = reinterpret_cast<float4*>(c.part_o + pr * D + 32 * cc);
+        for (int cc = 0; cc < 4; ++cc) tmem_ld_32_async(s_tmem + 32 * cc, x[cc]);
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
-                                   __uint_as_float(x[4 * e + 3]));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(out + 32 * cc);
+        for (int cc = 0; cc < 4; ++cc) {
+          tmem_wait_ld(x[cc]);
+          if (F8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = ptx::pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 32; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + 32 * cc + e);
+              x[cc][e] = __float_as_uint(__uint_as_float(x[cc][e]) * f.x);
+              x[cc][e + 1] = __float_as_uint(__uint_as_float(x[cc][e + 1]) * f.y);
+              x[cc][e + 2] = __float_as_uint(__uint_as_float(x[cc][e + 2]) * f.z);
+              x[cc][e + 3] = __float_as_uint(__uint_as_float(x[cc][e + 3]) * f.w);
             }
           }
+          if (!whole) {
+            const uint32_t vis = seen[grp * 4 + cc];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[cc][e] = (vis >> e) & 1u ? x[cc][e] : 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[cc][e]));
+        }
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        float before = m;
+        if (!two) {   // the other group's step comes first
+          if (q > 0) named_sync(4 + 2 * quarter + grp, 64);
+          before = q > 0 ? m_row[r] : -INFINITY;
+        }
+        const float mn = fmaxf(before, F8 || top == -INFINITY ? top : top * scale);
+        float now = before;
+        if (j == 0) {
+          now = mn;
+        } else if (__any_sync(0xffffffffu, mn - before > kLazy)) {
+          now = mn;
+          // O's last MMA: PV(q - 2) of two row tiles came before S(q)
+          if (!two) {
+            wait(pv_done, q - 1);
+            ptx::tc_fence_after();
+          }
+          const float f = before == now ? 1.f : ex2(before - now);
+          const uint32_t o_addr = o_tmem + (two ? grp * kTile : 0) + lanes;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t y[16];
+            tmem_ld_16_raw(o_addr + 16 * cc, y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+            tmem_st_16(o_addr + 16 * cc, y);
+          }
+          tmem_wait_st();
+        }
+        if (!two && q + 1 < steps) {
+          m_row[r] = now;
+          named_arrive(4 + 2 * quarter + (grp ^ 1), 64);
+        }
+        l *= m == now ? 1.f : ex2(m - now);
+        m = now;
+        const float base = m == -INFINITY ? 0.f : m;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float y = __uint_as_float(x[cc][e + k]);
+              p[k] = ex2(F8 ? y - base : fmaf(y, scale, -base));
+              l4[k] += p[k];
+            }
+            if (F8) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + 128 + 32 * cc + e);
+              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
+            }
+            w[e / 2] = ptx::pack_bf16x2(p[0], p[1]);
+            w[e / 2 + 1] = ptx::pack_bf16x2(p[2], p[3]);
+          }
+          tmem_st_16(s_tmem + 16 * cc, w);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_wait_st();
+      }
+      if (!whole && !(two && grp)) {
+        // hidden values become zeros: their weight is 0, and 0 times anything stored there must be 0
+        wait(&v_landed[grp], partial++);
+        if (!((seen[grp * 4 + quarter] >> lane) & 1u)) {
+          uint8_t* dst = ring + ((order.of_v(j) * NC + r / VK) % NST) * kStage + (r % VK) * 128;
+#pragma unroll 1
+          for (int k = 0; k < NC * 8; ++k)
+            *reinterpret_cast<uint4*>(dst + (k >> 3) * VK * 128 + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          ptx::fence_proxy_async_smem();
         }
       }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&p_ready[grp]);
+    }
+    // ---- output: rows staged where the tiles were, a bulk copy each -------------
+    if (n > 0) wait(o_done, 0);
+    ptx::tc_fence_after();
+    if (!two) {   // both groups' sums, in units of the last maximum; each writes half of the columns
+      float2* ml = reinterpret_cast<float2*>(Qs);
+      named_sync(1, 256);
+      ml[grp * 128 + r] = make_float2(m, l);
+      named_sync(1, 256);
+      const float2 other = ml[(grp ^ 1) * 128 + r];
+      named_sync(1, 256);                         // (the rows below are staged over this)
+      const float top = fmaxf(m, other.x);
+      l = l * (m == top ? 1.f : ex2(m - top)) + other.y * (other.x == top ? 1.f : ex2(other.x - top));
+      m = top;
+    }
+    const bool split = c.plan.n_slots > 1, first = two || grp == 0;
+    const long long pr = part_row(c, u, row);
+    if (mine && first && split) {
+      // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
+      const float mo = l != l ? INFINITY : l == 0.f ? -INFINITY : m;
+      *reinterpret_cast<float2*>(c.part_ml + pr * 2) = make_float2(mo, l);
+    }
+    if (mine && first && !split && c.lse)
+      c.lse[((long long)b * c.Tq + t_row) * c.Hq + h_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (live) {
+      const int cols = two ? D : D / 2, c0 = two ? 0 : grp * (D / 2);
+      uint8_t* stage = Qs + (tile_row + r) * C::kRowBytes + c0 * (split ? 4 : 2);
+#pragma unroll 1
+      for (int cc = 0; cc < cols; cc += 32) {
+        uint32_t x[32];
+        if (n > 0) {
+          tmem_ld_32_async(o_tmem + (two ? grp * kTile : 0) + lanes + c0 + cc, x);
+          tmem_wait_ld(x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0u;
+        }
+        if (split) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stage + cc * 4 + e * 16) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = ptx::pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + cc * 2 + e * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      if (mine) {
+        if (split) {
+          if (l != 0.f) bulk_store(c.part_o + pr * D + c0, stage, cols * 4);   // (the join does not read an empty part)
+        } else {
+          bulk_store(reinterpret_cast<__nv_bfloat16*>(c.out) + b * c.ob + t_row * c.ot + h_row * c.oh + c0, stage, cols * 2);
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
   ptx::tc_fence_before();
@@ -608,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, Cfg<D, F8>::kTwo ? 2 : 1
   }
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::TCOLS);
+    ptx::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -687,7 +755,7 @@ cudaError_t configure_attention_tc() {
   return e;
 }
 
-int attention_tc_ctas_per_sm(int D, bool f8) { return D <= 128 && !f8 ? 2 : 1; }
+int attention_tc_rows(int D) { return D == 256 ? 128 : 256; }
 
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st) {
   const bool f8 = (c.pre.len && c.pre_f8) || (c.own.len && c.own_f8);

@@ -414,7 +414,7 @@ cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_all(const AttnCall& c, cudaStream_t st) {
-  cudaError_t e = c.bf16 ? launch_attention_tc(c, st) : c.plan.bm == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
+  cudaError_t e = c.bf16 ? launch_attention_tc(c, st) : c.plan.bm_e == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
   if (e != cudaSuccess || c.plan.n_slots == 1) return e;
   return c.bf16 ? launch_combine<__nv_bfloat16, D>(c, st) : launch_combine<float, D>(c, st);
 }
@@ -462,19 +462,20 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   AttnPlan p{};
   p.rows_b = c.Tq * c.group;
   p.kt = c.bf16 ? 128 : kKeys;
-  p.bm = c.bf16 ? 128 : p.rows_b <= 16 ? 16 : 64;
-  const bool f8 = (c.pre.len > 0 && c.pre_f8) || (c.own.len > 0 && c.own_f8);
-  const int slots = num_sms * (c.bf16 ? attention_tc_ctas_per_sm(c.D, f8) : 2);   // CTAs that run at once
-  const int tb = (p.rows_b + p.bm - 1) / p.bm;
+  const int most = c.bf16 ? attention_tc_rows(c.D) : 64;             // rows of a CTA
+  const int slots = num_sms * (c.bf16 ? 1 : 2);                       // CTAs that run at once
+  p.bm_e = c.bf16 ? most : p.rows_b <= 16 ? 16 : 64;
+  p.bm_s = c.bf16 ? most : p.bm_e;
   // Rows of several elements share a tile (and its pass over the prefix) when
   // one element's rows would leave half of it empty.
-  const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= p.bm / 2;
+  const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : p.bm_e / 2);
+  const int tb = (p.rows_b + p.bm_e - 1) / p.bm_e;
   auto split = [&](long long units, int keys) {
     const int tiles = (keys + p.kt - 1) / p.kt;
     return (int)std::max(1LL, std::min<long long>({slots / (units * c.Hkv), tiles, 64}));
   };
   if (stack) {
-    p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm - 1) / p.bm);
+    p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm_s - 1) / p.bm_s);
     p.ns = split(p.tiles_s, c.pre.len);
   }
   p.prefix_in_elem = c.pre.len > 0 && !stack;

@@ -31,7 +31,7 @@ struct KvSource {
 // (prefix_in_elem) or of its own keys.  Each row has n_slots partial results
 // (slot = range), joined by combine_kernel when there is more than one.
 struct AttnPlan {
-  int bm;                      // rows of a unit
+  int bm_s, bm_e;              // rows of a stacked and of an element unit
   int kt;                      // keys of a tile
   int rows_b;                  // rows of one element: query tokens * group
   int tiles_s, ns;             // stacked units: row tiles, key ranges (0: none)
@@ -70,7 +70,7 @@ cudaError_t configure_attention();
 // The tensor-core kernel (bf16 queries).
 cudaError_t configure_attention_tc();
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st);
-int attention_tc_ctas_per_sm(int D, bool f8);
+int attention_tc_rows(int D);   // rows of a CTA
 
 // One tensor of rows [outer][batch][token][head][D] for the cache kernels;
 // strides in elements, the outer index (keys, values, or layers of both)
@@ -119,36 +119,42 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
   const AttnPlan& p = c.plan;
   AttnUnit u;
   u.kvh = blockIdx.y;
-  long long x = blockIdx.x;
-  const long long stacked = (long long)p.tiles_s * p.ns;
+  unsigned x = blockIdx.x;
+  const unsigned stacked = (unsigned)p.tiles_s * p.ns;
   int split, nsplit;
   if (x < stacked) {
-    const int tile = (int)(x % p.tiles_s);
-    split = (int)(x / p.tiles_s);
+    split = (int)(x / (unsigned)p.tiles_s);
+    const int tile = (int)(x - (unsigned)split * p.tiles_s);
     nsplit = p.ns;
     u.slot = split;
     u.b = 0;
-    u.row0 = (long long)tile * p.bm;
-    u.nrows = (int)min((long long)p.bm, (long long)c.B * p.rows_b - u.row0);
+    u.row0 = (long long)tile * p.bm_s;
+    u.nrows = (int)min((long long)p.bm_s, (long long)c.B * p.rows_b - u.row0);
     u.len0 = valid_len(c.pre, 0, c.status);
     u.len1 = 0;
   } else {
     x -= stacked;
-    const int tile = (int)(x % p.tiles_e);
-    x /= p.tiles_e;
-    split = (int)(x % p.ne);
+    const unsigned y = x / (unsigned)p.tiles_e;
+    const int tile = (int)(x - y * p.tiles_e);
+    u.b = (int)(y / (unsigned)p.ne);
+    split = (int)(y - (unsigned)u.b * p.ne);
     nsplit = p.ne;
-    u.b = (int)(x / p.ne);
     u.slot = p.ns + split;
-    u.row0 = (long long)u.b * p.rows_b + (long long)tile * p.bm;
-    u.nrows = min(p.bm, p.rows_b - tile * p.bm);
+    u.row0 = (long long)u.b * p.rows_b + (long long)tile * p.bm_e;
+    u.nrows = min(p.bm_e, p.rows_b - tile * p.bm_e);
     u.len0 = p.prefix_in_elem ? valid_len(c.pre, 0, c.status) : 0;
     u.len1 = valid_len(c.own, u.b, c.status);
   }
   u.n0 = (u.len0 + p.kt - 1) / p.kt;
-  const long long n = u.n0 + (u.len1 + p.kt - 1) / p.kt;
-  u.t0 = (int)(n * split / nsplit);
-  u.t1 = (int)(n * (split + 1) / nsplit);
+  const unsigned n = u.n0 + (u.len1 + p.kt - 1) / p.kt;
+  if (nsplit == 1) {
+    u.t0 = 0;
+    u.t1 = (int)n;
+  } else {
+    const unsigned each = n / (unsigned)nsplit, rest = n - each * nsplit;   // the first `rest` ranges take one tile more
+    u.t0 = (int)(each * split + min((unsigned)split, rest));
+    u.t1 = u.t0 + (int)each + ((unsigned)split < rest ? 1 : 0);
+  }
   return u;
 }
 
