@@ -99,6 +99,11 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
   d |= (uint64_t)2 << 61;
   return d;
 }
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
 constexpr uint32_t kBTransposed = 1u << 16;      // instruction descriptor: B is MN-major
 
 #define R8(o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
@@ -141,6 +146,35 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -223,7 +257,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint32_t* seen = (uint32_t*)(m_row + 128);      // [2 groups][4] visible keys of the group's tile
   float* scales = m_row + 256;                    // E4M3: [2 groups][2][K, V][128]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform)
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < NST; ++i) {
@@ -236,9 +271,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s_full[i], 1);
-      ptx::mbar_init(&p_ready[i], 128);
+      ptx::mbar_init(&p_ready[i], 4);
       ptx::mbar_init(&v_landed[i], 1);
-      ptx::mbar_init(&q_ready[i], 128);
+      ptx::mbar_init(&q_ready[i], 4);
     }
     ptx::mbar_init(pv_done, 1);
     ptx::mbar_init(o_done, 1);
@@ -256,7 +291,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   const uint32_t o_tmem = tmem + 2 * kTile;       // two S buffers, then O of each row tile
   // After a wait has run out every other one gives up at once, so that all
   // warps reach the end (and the barriers among them) without their data.
@@ -314,60 +349,92 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMAs --------------------------------------------------------------
+    // ---- MMAs: the whole warp walks the steps, one lane issues -----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       const uint32_t id_s = ptx::idesc_bf16_f32(128, kTile), id_o = ptx::idesc_bf16_f32(128, D) | kBTransposed;
       const uint64_t qd = ptx::sw128_kmajor_desc(ptx::smem_u32(Qs)), kd = ptx::sw128_kmajor_desc(ptx::smem_u32(ring));
       const uint64_t vd = sw128_mnmajor_desc(ptx::smem_u32(ring), VK * 128);
-      bool ok = wait(&q_ready[0], 0);
-      if (!two) ok = wait(&q_ready[1], 0) && ok;
-      for (int i = 0; i < 2 * steps && ok; ++i) {
-        // S(0), S(1), PV(0), S(2), PV(1), ..., PV(steps - 1)
-        const bool pv = i == 2 * steps - 1 || (i > 0 && !(i & 1));
-        const int q = pv ? (i == 2 * steps - 1 ? steps - 1 : (i >> 1) - 1) : (i + 1) >> 1;
-        const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
-        const bool last_use = !two || rt == 1;    // of the key tile's stages
-        const uint32_t s_tmem = tmem + buf * kTile;
-        if (!pv) {
-          // (S(q) is written over P(q - 2), whose MMA comes before it in this thread's order)
-          if (q == 1 && two && !(ok = wait(&q_ready[1], 0))) break;
-          int st = order.of_k(j) * NC;
-          for (int cc = 0; cc < NC && ok; ++cc, ++st) {
-            const int s = st % NST;
-            if (!(ok = wait(&ready[s], st / NST))) break;
-            ptx::tc_fence_after();
-            const uint64_t qa = qd + (uint64_t)((rt * C::QB + cc * 16384) >> 4), ka = kd + (uint64_t)(s * (kStage >> 4));
+      const bool leader = elect_one();
+      // tiles with hidden keys, as has_hidden says
+      const bool pre_mask = c.pre.mask != nullptr, own_mask = c.own.mask != nullptr;
+      const int pre_end = u.len0 % kTile ? u.n0 - 1 - u.t0 : -1;            // key tiles (of the unit) that end early
+      const int own_end = u.len1 % kTile ? u.n0 + u.len1 / kTile - u.t0 : -1, own0 = u.n0 - u.t0;
+      const uint32_t s_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32), q_lo = (uint32_t)qd, k_lo = (uint32_t)kd,
+                     v_lo = (uint32_t)vd;
+      bool ok = true;
+      // the NC stages of a load of the order, from its position
+      auto landed = [&](int pos) {
+        int s = (pos * NC) % NST, ph = (pos * NC) / NST;
+        for (int cc = 0; cc < NC; ++cc) {
+          ok = ok && wait(&ready[s], ph);
+          if (++s == NST) s = 0, ++ph;
+        }
+      };
+      auto scores = [&](int q) {                  // S(q), over P(q - 2), whose MMA comes before it in this thread's order
+        const int buf = q & 1, rt = two ? buf : 0;
+        int s = (order.of_k(two ? q >> 1 : q) * NC) % NST;
+        if (leader && ok) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) ptx::umma_bf16(s_tmem, qa + 2 * kk, ka + 2 * kk, id_s, (cc | kk) != 0);
-            if (last_use) ptx::umma_commit(&empty[s]);
+          for (int cc = 0; cc < NC; ++cc) {
+            const uint32_t qa = q_lo + rt * (C::QB >> 4) + cc * (16384 >> 4), ka = k_lo + s * (kStage >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::umma_bf16(tmem + buf * kTile, desc64(qa + 2 * kk, s_hi), desc64(ka + 2 * kk, s_hi), id_s, (cc | kk) != 0);
+            if (!two || rt == 1) ptx::umma_commit(&empty[s]);   // the key tile's last use
+            if (++s == NST) s = 0;
           }
-          if (ok) ptx::umma_commit(&s_full[buf]);
-        } else {
-          int st = order.of_v(j) * NC;
-          if (rt == 0 && has_hidden(c, tile_at(u, u.t0 + j))) {
-            for (int cc = 0; cc < NC && ok; ++cc) ok = wait(&ready[(st + cc) % NST], (st + cc) / NST);
-            if (!ok) break;
-            ptx::mbar_arrive(&v_landed[buf]);
-          }
-          if (!(ok = wait(&p_ready[buf], q >> 1))) break;
-          for (int cc = 0; cc < NC && ok; ++cc, ++st) {
-            const int s = st % NST;
-            if (!(ok = wait(&ready[s], st / NST))) break;
-            ptx::tc_fence_after();
-            const uint64_t va = vd + (uint64_t)(s * (kStage >> 4));
+          ptx::umma_commit(&s_full[buf]);
+        }
+      };
+      ok = wait(&q_ready[0], 0);
+      if (!two) ok = wait(&q_ready[1], 0) && ok;
+      landed(order.of_k(0));
+      ptx::tc_fence_after();
+      scores(0);
+      if (steps > 1) {
+        if (two) ok = wait(&q_ready[1], 0) && ok;
+        else landed(order.of_k(1));
+        ptx::tc_fence_after();
+        scores(1);
+      }
+      // What the ring holds at once: V(j) and the next K, unless it is small.
+      constexpr bool kAhead = 2 * NC <= NST;
+      for (int q = 0; q < steps && ok; ++q) {
+        const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
+        if (rt == 0) {
+          landed(order.of_v(j));
+          if (((j < own0 ? pre_mask : own_mask) || j == pre_end || j == own_end) && leader && ok) ptx::mbar_arrive(&v_landed[buf]);
+        }
+        const bool next = q + 2 < steps;
+        if (kAhead && next && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
+        ok = ok && wait(&p_ready[buf], q >> 1);
+        ptx::tc_fence_after();
+        int s = (order.of_v(j) * NC) % NST;
+        if (leader && ok) {
+#pragma unroll
+          for (int cc = 0; cc < NC; ++cc) {
+            const uint32_t va = v_lo + s * (kStage >> 4);
 #pragma unroll
             for (int kk = 0; kk < VK / 16; ++kk)
-              umma_bf16_ts(o_tmem + rt * kTile, s_tmem + (cc * VK + kk * 16) / 2, va + kk * (2048 >> 4), id_o,
-                           (j | cc | kk) != 0);
-            if (last_use) ptx::umma_commit(&empty[s]);
+              umma_bf16_ts(o_tmem + rt * kTile, tmem + buf * kTile + (cc * VK + kk * 16) / 2, desc64(va + kk * (2048 >> 4), v_hi),
+                           id_o, (j | cc | kk) != 0);
+            if (!two || rt == 1) ptx::umma_commit(&empty[s]);
+            if (++s == NST) s = 0;
           }
-          if (ok && !two) ptx::umma_commit(pv_done);
+          if (!two) ptx::umma_commit(pv_done);
+        }
+        if (next) {
+          if (!kAhead && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
+          ptx::tc_fence_after();
+          scores(q + 2);
         }
       }
       // every MMA completes before the tensor memory is read for the last time and freed
-      ptx::umma_commit(o_done);
-      if (!ptx::mbar_wait(o_done, 0, kDrainNs)) atomicOr(c.status, RTV_DEV_TIMEOUT);
+      if (leader) {
+        ptx::umma_commit(o_done);
+        if (!ptx::mbar_wait(o_done, 0, kDrainNs)) atomicOr(c.status, RTV_DEV_TIMEOUT);
+      }
     }
     __syncwarp();
   } else if (warp < C::kSoft || warp >= C::kSoft + 8) {
@@ -459,7 +526,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&q_ready[grp]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&q_ready[grp]);
     }
     const float scale = fabsf(c.scale_log2);
     float m = -INFINITY, l = 0.f;                 // l counts in units of 2^m
@@ -534,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if (q > 0) named_sync(4 + 2 * quarter + grp, 64);
           before = q > 0 ? m_row[r] : -INFINITY;
         }
-        const float mn = fmaxf(before, F8 || top == -INFINITY ? top : top * scale);
+        const float mn = fmaxf(before, F8 ? top : top * scale);
         float now = before;
         if (j == 0) {
           now = mn;
@@ -561,32 +629,38 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           m_row[r] = now;
           named_arrive(4 + 2 * quarter + (grp ^ 1), 64);
         }
-        l *= m == now ? 1.f : ex2(m - now);
-        m = now;
+        if (m != now) {                            // (the groups hand maxima on, or a rescale just above)
+          l *= ex2(m - now);
+          m = now;
+        }
         const float base = m == -INFINITY ? 0.f : m;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            float p[4];
+            float2 p[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float y = __uint_as_float(x[cc][e + k]);
-              p[k] = ex2(F8 ? y - base : fmaf(y, scale, -base));
-              l4[k] += p[k];
+            for (int k = 0; k < 2; ++k) {
+              const float2 y = make_float2(__uint_as_float(x[cc][e + 2 * k]), __uint_as_float(x[cc][e + 2 * k + 1]));
+              p[k] = F8 ? add2(y, base2) : fma2(y, scale2, base2);
+              p[k].x = ex2(p[k].x);
+              p[k].y = ex2(p[k].y);
+              l2[k] = add2(l2[k], p[k]);
             }
             if (F8) {
               const float4 f = *reinterpret_cast<const float4*>(sc + 128 + 32 * cc + e);
-              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
+              p[0] = mul2(p[0], make_float2(f.x, f.y));
+              p[1] = mul2(p[1], make_float2(f.z, f.w));
             }
-            w[e / 2] = ptx::pack_bf16x2(p[0], p[1]);
-            w[e / 2 + 1] = ptx::pack_bf16x2(p[2], p[3]);
+            w[e / 2] = ptx::pack_bf16x2(p[0].x, p[0].y);
+            w[e / 2 + 1] = ptx::pack_bf16x2(p[1].x, p[1].y);
           }
           tmem_st_16(s_tmem + 16 * cc, w);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         tmem_wait_st();
       }
       if (!whole && !(two && grp)) {
@@ -601,7 +675,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(&p_ready[grp]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&p_ready[grp]);
     }
     // ---- output: rows staged where the tiles were, a bulk copy each -------------
     if (n > 0) wait(o_done, 0);
