@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+  ptx::pdl_launch_dependents();                   // (tensor memory is allocated; combine_kernel waits for this grid's end)
   const uint32_t o_tmem = tmem + 2 * kTile;       // two S buffers, then O of each row tile
   // After a wait has run out every other one gives up at once, so that all
   // warps reach the end (and the barriers among them) without their data.
@@ -803,9 +804,10 @@ cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
   };
   int pre_b = 0;
   source(c.pre, c.pre_f8, 1, &m.pre_k, &m.pre_v, &m.pre_h, &pre_b);
-  source(c.own, c.own_f8, c.B, &m.own_k, &m.own_v, &m.own_h, &m.own_b);
+  if (!c.plan.decode) source(c.own, c.own_f8, c.B, &m.own_k, &m.own_v, &m.own_h, &m.own_b);
   if (!ok) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + (long long)c.B * c.plan.tiles_e * c.plan.ne), c.Hkv);
+  const long long elems = c.plan.decode ? 0 : (long long)c.B * c.plan.tiles_e * c.plan.ne;
+  const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + elems), c.Hkv);
   attn_cache_kernel<D, F8><<<grid, C::kThreads, C::kSmem, st>>>(c, m);
   return cudaGetLastError();
 }
@@ -833,7 +835,7 @@ cudaError_t configure_attention_tc() {
 int attention_tc_rows(int D) { return D == 256 ? 128 : 256; }
 
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st) {
-  const bool f8 = (c.pre.len && c.pre_f8) || (c.own.len && c.own_f8);
+  const bool f8 = (c.pre.len && c.pre_f8) || (!c.plan.decode && c.own.len && c.own_f8);
   if (f8)
     return c.D == 64 ? launch_tc<64, true>(c, st) : c.D == 128 ? launch_tc<128, true>(c, st) : launch_tc<256, true>(c, st);
   return c.D == 64 ? launch_tc<64, false>(c, st) : c.D == 128 ? launch_tc<128, false>(c, st) : launch_tc<256, false>(c, st);

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
   float* Ok = Ps + BM * LP;       // 1: the tile's key is seen
   const AttnUnit u = attn_unit(c);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  ptx::pdl_launch_dependents();   // (combine_kernel waits for this grid's end before it reads)
 
   for (int i = tid; i < BM * C4; i += 256) {
     const int r = i / C4, d = (i - r * C4) * 4;
@@ -330,48 +331,64 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
   }
 }
 
-// Join of a row's partial results: out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,
-// slots in order; a warp per row.  Empty parts (m = -inf) are not read.
+// Join of a row's partial results: out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k.
+// `per` warps share a row, each taking every per-th slot with its loads in
+// flight together; their sums are added in warp order.  Empty parts (m = -inf)
+// are not read.
 template <typename QT, int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnCall c) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnCall c, int per) {
   constexpr int V = D >= 128 ? 4 : 2, NC = D / (32 * V);   // elements of a lane's load, loads of a lane
+  __shared__ float sums[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
   const long long rows = (long long)c.B * c.plan.rows_b;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int kvh = blockIdx.y, lane = threadIdx.x & 31, n = c.plan.n_slots;
-  ptx::pdl_wait();
-  if (row >= rows) return;
+  const long long row = (long long)blockIdx.x * (8 / per) + warp / per;
+  const int kvh = blockIdx.y, n = c.plan.n_slots;
+  const bool real = row < rows;
   const long long base = (long long)kvh * n * rows + row;
-  float top = -INFINITY;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, c.part_ml[(base + k * rows) * 2]);
-  top = warp_max(top);
+  ptx::pdl_wait();
+  float top = -INFINITY, sum = 0.f;
   float acc[NC][V] = {};
-  float sum = 0.f;
-  if (top != -INFINITY) {
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < n) ml = *reinterpret_cast<const float2*>(c.part_ml + (base + (k0 + lane) * rows) * 2);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-      sum += ml.x == -INFINITY ? 0.f : w * ml.y;
-      const int kn = min(32, n - k0);
-#pragma unroll 4
-      for (int k = 0; k < kn; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k), mk = __shfl_sync(0xffffffffu, ml.x, k);
-        if (mk == -INFINITY) continue;
-        const float* src = c.part_o + (base + (k0 + k) * rows) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          float v[V];
-          if (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + 32 * V * i);
-          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src + 32 * V * i);
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[i][e] = fmaf(wk, v[e], acc[i][e]);
-        }
-      }
+  if (real) {
+    const float2* ml = reinterpret_cast<const float2*>(c.part_ml) + base;
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, ml[k * rows].x);
+    top = warp_max(top);
+    for (int k = lane; k < n; k += 32) {
+      const float2 x = ml[k * rows];
+      if (x.x != -INFINITY) sum += exp2f(x.x - top) * x.y;
     }
     sum = warp_sum(sum);
+#pragma unroll 4
+    for (int k = sub; k < n; k += per) {
+      const float mk = ml[k * rows].x;
+      if (mk == -INFINITY) continue;
+      const float w = exp2f(mk - top);
+      const float* src = c.part_o + (base + k * rows) * D + lane * V;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float v[V];
+        if (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + 32 * V * i);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src + 32 * V * i);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[i][e] = fmaf(w, v[e], acc[i][e]);
+      }
+    }
   }
-  const long long b = row / c.plan.rows_b;
-  const int rr = (int)(row - b * c.plan.rows_b), t = rr / c.group, h = kvh * c.group + rr - t * c.group;
+  if (per > 1) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sums[warp][32 * V * i + lane * V + e] = acc[i][e];
+    __syncthreads();
+    if (sub == 0)
+      for (int k = 1; k < per; ++k)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[i][e] += sums[warp + k][32 * V * i + lane * V + e];
+  }
+  if (!real || sub) return;
+  const unsigned b = (unsigned)row / (unsigned)c.plan.rows_b, rr = (unsigned)row - b * (unsigned)c.plan.rows_b;
+  const unsigned t = rr / (unsigned)c.group, h = kvh * c.group + rr - t * (unsigned)c.group;
   const float inv = top == -INFINITY ? 0.f : 1.f / sum;
   QT* dst = reinterpret_cast<QT*>(c.out) + b * c.ob + t * c.ot + h * c.oh + lane * V;
 #pragma unroll
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     }
   }
   if (c.lse && lane == 0)
-    c.lse[(b * c.Tq + t) * c.Hq + h] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    c.lse[((long long)b * c.Tq + t) * c.Hq + h] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int BM>
@@ -401,7 +418,8 @@ cudaError_t launch_f32(const AttnCall& c, cudaStream_t st) {
 template <typename QT, int D>
 cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)c.B * c.plan.rows_b + 7) / 8), c.Hkv);
+  const int per = c.plan.n_slots >= 16 ? 8 : c.plan.n_slots >= 4 ? 2 : 1;   // warps of a row
+  cfg.gridDim = dim3((unsigned)(((long long)c.B * c.plan.rows_b * per + 7) / 8), c.Hkv);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -409,12 +427,18 @@ cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<QT, D>, c);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<QT, D>, c, per);
 }
 
 template <int D>
-cudaError_t launch_all(const AttnCall& c, cudaStream_t st) {
-  cudaError_t e = c.bf16 ? launch_attention_tc(c, st) : c.plan.bm_e == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
+cudaError_t launch_all(AttnCall& c, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (!c.bf16) e = c.plan.bm_e == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
+  if (c.bf16 && (c.plan.ns || !c.plan.decode)) e = launch_attention_tc(c, st);
+  if (e == cudaSuccess && c.plan.decode && c.plan.ne) {
+    c.unit0 = (unsigned)c.plan.tiles_s * c.plan.ns;
+    e = launch_attention_decode(c, st);
+  }
   if (e != cudaSuccess || c.plan.n_slots == 1) return e;
   return c.bf16 ? launch_combine<__nv_bfloat16, D>(c, st) : launch_combine<float, D>(c, st);
 }
@@ -461,29 +485,39 @@ cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
 AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   AttnPlan p{};
   p.rows_b = c.Tq * c.group;
-  p.kt = c.bf16 ? 128 : kKeys;
+  p.cluster = 1;
+  // The few-row kernel reads one type; a prefix and own keys meet in it only without stacking.
+  p.decode = c.bf16 && p.rows_b <= kDecodeRows && (c.B > 1 || !c.pre.len || !c.own.len || c.pre_f8 == c.own_f8);
   const int most = c.bf16 ? attention_tc_rows(c.D) : 64;             // rows of a CTA
-  const int slots = num_sms * (c.bf16 ? 1 : 2);                       // CTAs that run at once
-  p.bm_e = c.bf16 ? most : p.rows_b <= 16 ? 16 : 64;
+  p.bm_e = p.decode ? kDecodeRows : c.bf16 ? most : p.rows_b <= 16 ? 16 : 64;
   p.bm_s = c.bf16 ? most : p.bm_e;
+  p.kt_s = c.bf16 ? 128 : kKeys;
+  p.kt_e = p.decode ? kDecodeTile : p.kt_s;
   // Rows of several elements share a tile (and its pass over the prefix) when
   // one element's rows would leave half of it empty.
   const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : p.bm_e / 2);
   const int tb = (p.rows_b + p.bm_e - 1) / p.bm_e;
-  auto split = [&](long long units, int keys) {
-    const int tiles = (keys + p.kt - 1) / p.kt;
+  // key ranges of `units` x heads units so that `slots` CTAs run at once
+  auto split = [&](long long units, int keys, int kt, int slots) {
+    const int tiles = (keys + kt - 1) / kt;
     return (int)std::max(1LL, std::min<long long>({slots / (units * c.Hkv), tiles, 64}));
   };
   if (stack) {
     p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm_s - 1) / p.bm_s);
-    p.ns = split(p.tiles_s, c.pre.len);
+    p.ns = split(p.tiles_s, c.pre.len, p.kt_s, c.bf16 ? num_sms : 2 * num_sms);
   }
   p.prefix_in_elem = c.pre.len > 0 && !stack;
   if (!stack || c.own.len > 0) {
+    const int keys = c.own.len + (p.prefix_in_elem ? c.pre.len : 0);
     p.tiles_e = tb;
-    p.ne = split((long long)c.B * tb, c.own.len + (p.prefix_in_elem ? c.pre.len : 0));
+    p.ne = split((long long)c.B * tb, keys, p.kt_e, p.decode ? attention_decode_ctas(c.D) * num_sms : c.bf16 ? num_sms : 2 * num_sms);
+    // Up to eight ranges join in a cluster, without a second launch.
+    if (p.decode && !stack && p.ne > 1) {
+      if (p.ne <= 16) p.ne = std::min(p.ne, 8);
+      if (p.ne <= 8) p.cluster = p.ne;
+    }
   }
-  p.n_slots = p.ns + p.ne;
+  p.n_slots = p.cluster > 1 ? 1 : p.ns + p.ne;
   return p;
 }
 
@@ -502,6 +536,7 @@ cudaError_t configure_attention() {
   chain(set_smem<256, 16>());
   chain(set_smem<256, 64>());
   chain(configure_attention_tc());
+  chain(configure_attention_decode());
   return e;
 }
 

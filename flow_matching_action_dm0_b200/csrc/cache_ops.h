@@ -25,19 +25,22 @@ struct KvSource {
 
 // How an attention call is split over CTAs.  A "row" is one (query token,
 // query head) of a KV head's group: row r of element b is token r / group,
-// head kvh * group + r % group.  Stacked units take 128 (tensor cores) or
-// BM (fp32) consecutive rows of the whole batch over a range of the prefix;
-// element units take rows of one element over a range of [prefix ; own keys]
-// (prefix_in_elem) or of its own keys.  Each row has n_slots partial results
-// (slot = range), joined by combine_kernel when there is more than one.
+// head kvh * group + r % group.  Stacked units take bm_s consecutive rows of
+// the whole batch over a range of the prefix; element units take bm_e rows of
+// one element over a range of [prefix ; own keys] (prefix_in_elem) or of its
+// own keys.  Each row has n_slots partial results (slot = range), joined by
+// combine_kernel when there is more than one; the ranges of a decode unit
+// that form a cluster join in it and count as one.
 struct AttnPlan {
   int bm_s, bm_e;              // rows of a stacked and of an element unit
-  int kt;                      // keys of a tile
+  int kt_s, kt_e;              // keys of their tiles
   int rows_b;                  // rows of one element: query tokens * group
   int tiles_s, ns;             // stacked units: row tiles, key ranges (0: none)
   int tiles_e, ne;             // element units: row tiles per element, key ranges (0: none)
   int prefix_in_elem;          // element units read the prefix too
-  int n_slots;                 // ns + ne
+  int decode;                  // element units are the few-row kernel's
+  int cluster;                 // its CTAs that join by distributed shared memory (1: none)
+  int n_slots;                 // partial results of a row
 };
 
 struct AttnCall {
@@ -53,6 +56,7 @@ struct AttnCall {
   KvSource pre, own;
   int pre_f8, own_f8;
   AttnPlan plan;
+  unsigned unit0;              // first unit of a launch
   float* part_o;               // [Hkv][n_slots][B * rows_b][D] unnormalised rows (n_slots > 1)
   float* part_ml;              // [Hkv][n_slots][B * rows_b][2] their maximum (base 2) and sum
   unsigned* status;
@@ -71,6 +75,11 @@ cudaError_t configure_attention();
 cudaError_t configure_attention_tc();
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st);
 int attention_tc_rows(int D);   // rows of a CTA
+// The few-row kernel (bf16 queries, 16 rows of an element or less).
+cudaError_t configure_attention_decode();
+cudaError_t launch_attention_decode(const AttnCall& c, cudaStream_t st);
+constexpr int kDecodeRows = 16, kDecodeTile = 64;
+constexpr int attention_decode_ctas(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }   // CTAs of an SM
 
 // One tensor of rows [outer][batch][token][head][D] for the cache kernels;
 // strides in elements, the outer index (keys, values, or layers of both)
@@ -119,10 +128,11 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
   const AttnPlan& p = c.plan;
   AttnUnit u;
   u.kvh = blockIdx.y;
-  unsigned x = blockIdx.x;
+  unsigned x = blockIdx.x + c.unit0;
   const unsigned stacked = (unsigned)p.tiles_s * p.ns;
-  int split, nsplit;
+  int split, nsplit, kt;
   if (x < stacked) {
+    kt = p.kt_s;
     split = (int)(x / (unsigned)p.tiles_s);
     const int tile = (int)(x - (unsigned)split * p.tiles_s);
     nsplit = p.ns;
@@ -134,19 +144,20 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
     u.len1 = 0;
   } else {
     x -= stacked;
+    kt = p.kt_e;
     const unsigned y = x / (unsigned)p.tiles_e;
     const int tile = (int)(x - y * p.tiles_e);
     u.b = (int)(y / (unsigned)p.ne);
     split = (int)(y - (unsigned)u.b * p.ne);
     nsplit = p.ne;
-    u.slot = p.ns + split;
+    u.slot = p.n_slots > 1 ? p.ns + split : 0;
     u.row0 = (long long)u.b * p.rows_b + (long long)tile * p.bm_e;
     u.nrows = min(p.bm_e, p.rows_b - tile * p.bm_e);
     u.len0 = p.prefix_in_elem ? valid_len(c.pre, 0, c.status) : 0;
     u.len1 = valid_len(c.own, u.b, c.status);
   }
-  u.n0 = (u.len0 + p.kt - 1) / p.kt;
-  const unsigned n = u.n0 + (u.len1 + p.kt - 1) / p.kt;
+  u.n0 = (u.len0 + kt - 1) / kt;
+  const unsigned n = u.n0 + (u.len1 + kt - 1) / kt;
   if (nsplit == 1) {
     u.t0 = 0;
     u.t1 = (int)n;
