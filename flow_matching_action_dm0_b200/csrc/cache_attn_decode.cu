@@ -1,20 +1,21 @@
 // bf16 attention over key/value caches for few rows (single tokens: 16 rows
 // or less of an element's KV head group), bf16 or E4M3 caches.
 //
-// Bound by the bytes of the cache, which are read once, straight into
-// registers in the layout of the warp-level matrix instruction (m16n8k16, fp32
-// accumulate), with no pass through shared memory:
+// Bound by the bytes of the cache, which are read once, by a ring of
+// asynchronous copies of each warp's own (16 keys a stage, hidden keys filled
+// with zeros and not read), and multiplied by the warp-level matrix
+// instruction (m16n8k16, fp32 accumulate):
 //   S = Q K^T    the order of the dims in a dot product is free, so lane
-//                (n, c) reads 16 neighbouring dims of key n in each 64 and
+//                (n, c) takes 16 neighbouring dims of key n in each 64 and
 //                they are four k-steps of its B fragment;
-//   O = P V      lane (n, c) reads 8 neighbouring dims of its four keys, and
+//   O = P V      lane (n, c) takes 8 neighbouring dims of its four keys, and
 //                the eight of them are eight column tiles of its B fragment
 //                (an output column stands for another dim, undone on writing).
-// Each warp takes 16 of the 64 keys of a tile with a running maximum of its
-// own (raised, and O rescaled, when it has grown by more than 8 in base 2);
-// the warps, and the CTAs of a cluster that share a row's keys, join at the
-// end, in order.  Keys that are hidden are not read at all.
-#include <type_traits>
+// A group takes 16 keys of a tile with a running maximum of its own (raised,
+// and O rescaled, when it has grown by more than 8 in base 2); at head_dim
+// 256 it is two warps, each with half of the dims, that add their scores.
+// The groups, and the CTAs of a cluster that share a row's keys, join at the
+// end, in order.
 
 #include "cache_ops.h"
 #include "common.cuh"
@@ -24,14 +25,28 @@ namespace rtv {
 
 namespace {
 
-constexpr int kRows = 16, kWarps = 4, kTile = 16 * kWarps;
+constexpr int kRows = 16;
 constexpr float kLazy = 8.f;
 
-__host__ __device__ constexpr int q_row_bytes(int d) { return d * 2 + 16; }   // fragment reads of 8 lanes hit all banks
-__host__ __device__ constexpr int o_row_floats(int d) { return d + 4; }
-__host__ __device__ constexpr int decode_smem(int d) {
-  return kRows * q_row_bytes(d) + kWarps * kRows * (o_row_floats(d) + 2) * 4 + kRows * 8;
-}
+template <int D, bool F8>
+struct Cfg {
+  static constexpr int HV = D == 256 ? 2 : 1;             // warps of a group: each has DW dims
+  static constexpr int DW = D / HV, NI = DW / 64;
+  static constexpr int G = decode_groups(D);              // groups of a CTA
+  static constexpr int kThreads = 32 * G * HV;
+  static constexpr int EB = F8 ? 1 : 2;
+  static constexpr int CPR = DW * EB / 16;                // 16-byte chunks of a key's row
+  static constexpr int kRow = DW * EB, kTileBytes = 16 * kRow;
+  static constexpr int kStage = 2 * kTileBytes + 160;     // K, V, 16 + 16 scales, visible keys
+  static constexpr int NST = F8 ? 4 : D == 64 ? 3 : 2;       // a warp's stages
+  static constexpr int kQRow = D * 2 + 16;                // fragment reads of 8 lanes hit all banks
+  static constexpr int LO = D + 4;                        // floats of a staged output row
+  static constexpr int kRing = G * HV * NST * kStage;
+  static constexpr int kJoin = G * kRows * (LO + 2) * 4 + kRows * 8;
+  static constexpr int kMain = kRing > kJoin ? kRing : kJoin;   // the join is staged over the ring
+  static constexpr int kExchange = HV == 2 ? G * 2 * 32 * 32 : 0;   // scores of each half
+  static constexpr int kSmem = kRows * kQRow + kMain + kExchange;
+};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -46,20 +61,72 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
   return ptx::pack_bf16x2(f.x, f.y);
 }
 
+// `bytes` of 16 (16-byte chunks) or 4 from global to shared memory; nothing is read, and zeros written, unless `on`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 template <int D, bool F8>
-__global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D))
     attn_decode_kernel(const __grid_constant__ AttnCall c, int cluster) {
-  constexpr int NI = D / 64, LO = o_row_floats(D);
+  using C = Cfg<D, F8>;
+  constexpr int NI = C::NI, LO = C::LO, G = C::G, HV = C::HV, CPR = C::CPR, NST = C::NST;
   extern __shared__ __align__(16) uint8_t sm[];
   uint8_t* Qs = sm;
-  float* Os = reinterpret_cast<float*>(sm + kRows * q_row_bytes(D));   // [kWarps][kRows][LO]
-  float2* ML = reinterpret_cast<float2*>(Os + kWarps * kRows * LO);    // [kWarps][kRows] maximum and sum
-  float2* Joined = ML + kWarps * kRows;                                // [kRows] of the CTA
+  uint8_t* main_sm = sm + kRows * C::kQRow;
+  float* Os = reinterpret_cast<float*>(main_sm);                       // [G][kRows][LO], after the loop
+  float2* ML = reinterpret_cast<float2*>(Os + G * kRows * LO);         // [G][kRows] maximum and sum
+  float2* Joined = ML + G * kRows;                                     // [kRows] of the CTA
   const AttnUnit u = attn_unit(c);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, cc = lane & 3;
+  const int grp = warp % G, half = warp / G, d0 = half * C::DW;        // the warp's keys and dims
   ptx::pdl_launch_dependents();   // (combine_kernel waits for this grid's end before it reads)
+  uint8_t* ring = main_sm + warp * NST * C::kStage;
+  const uint32_t ring_a = ptx::smem_u32(ring);
 
-  for (int i = tid; i < kRows * (D / 8); i += 32 * kWarps) {
+  // Where chunk ch of key k lies in a stage's tile: permuted so that the
+  // fragment reads of K (two keys a phase) and of V (four) hit all banks.
+  auto place = [&](int k, int ch) { return k * C::kRow + ((ch ^ (((((k >> 1) & 3) * 2) ^ ((k & 1) * (F8 ? 4 : 1))) & (CPR - 1))) << 4); };
+  // Asks for the warp's 16 keys of a tile; one commit group a tile.
+  auto request = [&](int tile, int slot) {
+    if (tile < u.t1) {
+      const bool pre = tile < u.n0;
+      const int k0 = (pre ? tile : tile - u.n0) * (16 * G) + 16 * grp, len = pre ? u.len0 : u.len1;
+      const long long st = pre ? c.pre.st : c.own.st;
+      const long long base = (pre ? 0 : u.b * c.own.sb) + (long long)k0 * st + u.kvh * (pre ? c.pre.sh : c.own.sh) + d0;
+      const uint8_t* mask = pre ? c.pre.mask : c.own.mask ? c.own.mask + u.b * c.own.mask_sb : nullptr;
+      const char* kp = reinterpret_cast<const char*>(pre ? c.pre.k : c.own.k);
+      const char* vp = reinterpret_cast<const char*>(pre ? c.pre.v : c.own.v);
+      const int key = lane & 15;
+      const bool see = k0 + key < len && (!mask || mask[k0 + key]);
+      const uint32_t bits = __ballot_sync(0xffffffffu, see) & 0xFFFFu;
+      const uint32_t dst = ring_a + slot * C::kStage;
+#pragma unroll
+      for (int i = 0; i < CPR / 2; ++i) {
+        const int k = i * (32 / CPR) + lane / CPR, ch = lane % CPR;
+        const bool on = (bits >> k) & 1u;
+        const long long off = on ? C::EB * (base + (long long)k * st) + ch * 16 : 0;
+        copy16(dst + place(k, ch), kp + off, on);
+        copy16(dst + C::kTileBytes + place(k, ch), vp + off, on);
+      }
+      if (F8) {
+        const long long off = (pre ? 0 : u.b * c.own.fb) + u.kvh * (pre ? c.pre.fh : c.own.fh) + (long long)(k0 + key) * (pre ? c.pre.ft : c.own.ft);
+        copy4(dst + 2 * C::kTileBytes + lane * 4, (lane < 16 ? (pre ? c.pre.ks : c.own.ks) : (pre ? c.pre.vs : c.own.vs)) + (see ? off : 0), see);
+      }
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * C::kStage + 2 * C::kTileBytes + 128) = bits;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) request(u.t0 + i, i);
+
+  for (int i = tid; i < kRows * (D / 8); i += C::kThreads) {
     const int r = i / (D / 8), ch = i - r * (D / 8);
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (r < u.nrows) {
@@ -67,84 +134,25 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
       v = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + u.b * c.qb + t * c.qt +
                                           (long long)(u.kvh * c.group + g) * c.qh + ch * 8);
     }
-    *reinterpret_cast<uint4*>(Qs + r * q_row_bytes(D) + ch * 16) = v;
+    *reinterpret_cast<uint4*>(Qs + r * C::kQRow + ch * 16) = v;
   }
   __syncthreads();
 
-  float o[D / 8][4];
+  float o[NI * 8][4];
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  for (int j = 0; j < NI * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows n and n + 8
   const float scale = c.scale_log2;
-  // One source's type holds for the whole unit; a tile is described by where
-  // its 16 keys of this warp begin.
-  struct Tile {
-    const char *k, *v;
-    long long base, st;
-    uint32_t bits[2];                               // key k of the first and second eight is seen: bit 4k
-    float ks[2], vs[2];                             // E4M3: scales of keys n and n + 8
-  };
-  constexpr int EB = F8 ? 1 : 2, KW = F8 ? 1 : 2;
-  uint4 kr[2][NI][KW];                              // K of the next tile to be scored
-  Tile cur{}, nxt{};
-  // Looks a tile up and asks for its keys: 16 dims of each 64 for the lane's two keys.
-  auto begin = [&](int tile, Tile& t) {
-    t.bits[0] = t.bits[1] = 0u;
-    if (tile >= u.t1) return;
-    const bool pre = tile < u.n0;
-    const int k0 = (pre ? tile : tile - u.n0) * kTile + 16 * warp, len = pre ? u.len0 : u.len1;
-    if (k0 >= len) return;
-    t.st = pre ? c.pre.st : c.own.st;
-    t.base = (pre ? 0 : u.b * c.own.sb) + (long long)k0 * t.st + u.kvh * (pre ? c.pre.sh : c.own.sh);
-    t.k = reinterpret_cast<const char*>(pre ? c.pre.k : c.own.k);
-    t.v = reinterpret_cast<const char*>(pre ? c.pre.v : c.own.v);
-    const uint8_t* mask = pre ? c.pre.mask : c.own.mask ? c.own.mask + u.b * c.own.mask_sb : nullptr;
-    const long long fb = (pre ? 0 : u.b * c.own.fb) + u.kvh * (pre ? c.pre.fh : c.own.fh), ft = pre ? c.pre.ft : c.own.ft;
-    const float *kf = pre ? c.pre.ks : c.own.ks, *vf = pre ? c.pre.vs : c.own.vs;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = k0 + n + 8 * h;
-      const bool see = k < len && (!mask || mask[k]);
-      t.bits[h] = __ballot_sync(0xffffffffu, see);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          kr[h][i][w] = make_uint4(0u, 0u, 0u, 0u);
-          if (see)
-            kr[h][i][w] =
-                __ldcs(reinterpret_cast<const uint4*>(t.k + EB * (t.base + (long long)(n + 8 * h) * t.st + 64 * i + 16 * cc)) + w);
-        }
-      t.ks[h] = t.vs[h] = 1.f;
-      if (F8 && see) {
-        t.ks[h] = kf[fb + (long long)k * ft];
-        t.vs[h] = vf[fb + (long long)k * ft];
-      }
-    }
-  };
-  begin(u.t0, nxt);
+  int slot = 0;
   for (int tile = u.t0; tile < u.t1; ++tile) {
-    cur = nxt;
-    if ((cur.bits[0] | cur.bits[1]) == 0u) {        // (the same in every lane)
-      begin(tile + 1, nxt);
-      continue;
-    }
-    // V: 8 dims of each 64 for the lane's four keys, 2c, 2c + 1, then + 8
-    using VT = typename std::conditional<F8, uint2, uint4>::type;
-    VT vr[NI][4];
-    auto load_v = [&](int i) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = 2 * cc + (q & 1);
-        vr[i][q] = VT{};
-        if ((cur.bits[q >> 1] >> (4 * k)) & 1u)
-          vr[i][q] = __ldcs(reinterpret_cast<const VT*>(cur.v + EB * (cur.base + (long long)(k + 8 * (q >> 1)) * cur.st + 64 * i + 8 * n)));
-      }
-    };
-    constexpr int NV = D == 256 && !F8 ? 1 : NI;    // V chunks asked for ahead of the scores
-#pragma unroll
-    for (int i = 0; i < NV; ++i) load_v(i);
-    const uint32_t bits[2] = {cur.bits[0], cur.bits[1]};
+    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+    __syncwarp();
+    const uint8_t* stage = ring + slot * C::kStage;
+    const uint32_t bits = *reinterpret_cast<const uint32_t*>(stage + 2 * C::kTileBytes + 128);
+    // the slot that was used last is free: every lane is past it
+    request(tile + NST - 1, slot == 0 ? NST - 1 : slot - 1);
+    slot = slot + 1 == NST ? 0 : slot + 1;
+    if (bits == 0u) continue;                       // (the same in the warps of a group)
 
     float s[2][4];
 #pragma unroll
@@ -152,43 +160,59 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       // Q rows n and n + 8, dims 64 i + 16 c ..: four k-steps of the A fragment
-      const uint8_t* qa = Qs + n * q_row_bytes(D) + (64 * i + 16 * cc) * 2;
+      const uint8_t* qa = Qs + n * C::kQRow + (d0 + 64 * i + 16 * cc) * 2;
       const uint4 q0 = *reinterpret_cast<const uint4*>(qa), q1 = *reinterpret_cast<const uint4*>(qa + 16);
-      const uint4 q2 = *reinterpret_cast<const uint4*>(qa + 8 * q_row_bytes(D)),
-                  q3 = *reinterpret_cast<const uint4*>(qa + 8 * q_row_bytes(D) + 16);
+      const uint4 q2 = *reinterpret_cast<const uint4*>(qa + 8 * C::kQRow), q3 = *reinterpret_cast<const uint4*>(qa + 8 * C::kQRow + 16);
       const uint32_t a[4][4] = {{q0.x, q2.x, q0.y, q2.y}, {q0.z, q2.z, q0.w, q2.w}, {q1.x, q3.x, q1.y, q3.y}, {q1.z, q3.z, q1.w, q3.w}};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t b[8];
+        const int k = n + 8 * h;
         if (F8) {
-          const uint32_t w[4] = {kr[h][i][0].x, kr[h][i][0].y, kr[h][i][0].z, kr[h][i][0].w};
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + place(k, 4 * i + cc));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 8; ++e) b[e] = e4m3x2_to_bf16x2((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
         } else {
-          b[0] = kr[h][i][0].x, b[1] = kr[h][i][0].y, b[2] = kr[h][i][0].z, b[3] = kr[h][i][0].w;
-          b[4] = kr[h][i][KW - 1].x, b[5] = kr[h][i][KW - 1].y, b[6] = kr[h][i][KW - 1].z, b[7] = kr[h][i][KW - 1].w;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + place(k, 8 * i + 2 * cc));
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + place(k, 8 * i + 2 * cc + 1));
+          b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w, b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) ptx::mma_bf16_16816(s[h], a[t], b[2 * t], b[2 * t + 1]);
       }
     }
-    begin(tile + 1, nxt);                           // its keys arrive while this tile's values are used
-    // scores of rows n, n + 8 with keys 2c, 2c + 1 (+ 8 h)
-    float top[2] = {-INFINITY, -INFINITY}, vw[2][2];
+    if (HV == 2) {   // the halves' scores, added in the same order by both
+      float4* ex = reinterpret_cast<float4*>(main_sm + C::kMain) + (size_t)grp * 2 * 64;
+      ex[half * 64 + lane] = make_float4(s[0][0], s[0][1], s[0][2], s[0][3]);
+      ex[half * 64 + 32 + lane] = make_float4(s[1][0], s[1][1], s[1][2], s[1][3]);
+      named_sync(1 + grp, 64);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = ex[32 * h + lane], y = ex[64 + 32 * h + lane];
+        s[h][0] = x.x + y.x, s[h][1] = x.y + y.y, s[h][2] = x.z + y.z, s[h][3] = x.w + y.w;
+      }
+      named_sync(1 + grp, 64);
+    }
+    // scores of rows n, n + 8 with keys 2c, 2c + 1 (+ 8 h)
+    float top[2] = {-INFINITY, -INFINITY};
+    const float* sc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes);
+    float2 vw[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 kw = F8 ? *reinterpret_cast<const float2*>(sc + 8 * h + 2 * cc) : make_float2(1.f, 1.f);
+      vw[h] = F8 ? *reinterpret_cast<const float2*>(sc + 16 + 8 * h + 2 * cc) : make_float2(1.f, 1.f);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int k = 2 * cc + e;
-        const bool on = (bits[h] >> (4 * k)) & 1u;
-        const float f = F8 ? __shfl_sync(0xffffffffu, cur.ks[h], 4 * k) * scale : scale;
-        vw[h][e] = F8 ? __shfl_sync(0xffffffffu, cur.vs[h], 4 * k) : 1.f;
+        const bool on = (bits >> (8 * h + 2 * cc + e)) & 1u;
+        const float f = F8 ? (e ? kw.y : kw.x) * scale : scale;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           s[h][2 * r + e] = on ? s[h][2 * r + e] * f : -INFINITY;
           top[r] = fmaxf(top[r], s[h][2 * r + e]);
         }
       }
+    }
     bool grow = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -203,7 +227,7 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
         m[r] = top[r];
         l[r] *= f;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
+        for (int j = 0; j < NI * 8; ++j) {
           o[j][2 * r] *= f;
           o[j][2 * r + 1] *= f;
         }
@@ -221,8 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
           for (int e = 0; e < 2; ++e) {
             const float x = ex2(s[h][2 * r + e] - b);
             l[r] += x;
-            // (a hidden key's value is not read, so its scale must not count either)
-            w[h][2 * r + e] = F8 ? ((bits[h] >> (4 * (2 * cc + e))) & 1u ? x * vw[h][e] : 0.f) : x;
+            w[h][2 * r + e] = F8 ? x * (e ? vw[h].y : vw[h].x) : x;   // (a hidden key's scale was filled with 0)
           }
       }
       p[0] = ptx::pack_bf16x2(w[0][0], w[0][1]);
@@ -232,13 +255,18 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (i + 1 >= NV && i + 1 < NI) load_v(i + 1);
-      uint32_t v[4][4];                             // [key][dims 2w, 2w + 1]
+      uint32_t v[4][4];                             // keys 2c, 2c + 1, then + 8; dims 2w, 2w + 1 of 8
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&vr[i][q]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[q][e] = F8 ? e4m3x2_to_bf16x2((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : w[F8 ? 0 : e];
+        const int k = 2 * cc + (q & 1) + 8 * (q >> 1);
+        if (F8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kTileBytes + place(k, 4 * i + (n >> 1)) + (n & 1) * 8);
+          v[q][0] = e4m3x2_to_bf16x2(x.x & 0xFFFFu), v[q][1] = e4m3x2_to_bf16x2(x.x >> 16);
+          v[q][2] = e4m3x2_to_bf16x2(x.y & 0xFFFFu), v[q][3] = e4m3x2_to_bf16x2(x.y >> 16);
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + C::kTileBytes + place(k, 8 * i + n));
+          v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+        }
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -247,17 +275,19 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();                                  // (the join is staged over the rings)
 
-  // ---- join of the warps -------------------------------------------------------
+  // ---- join of the groups -------------------------------------------------------
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     const int row = n + 8 * r;
     // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
-    if (cc == 0) ML[warp * kRows + row] = make_float2(l[r] != l[r] ? INFINITY : l[r] == 0.f ? -INFINITY : m[r], l[r]);
+    if (cc == 0 && half == 0) ML[grp * kRows + row] = make_float2(l[r] != l[r] ? INFINITY : l[r] == 0.f ? -INFINITY : m[r], l[r]);
     if (row < u.nrows) {
-      float* dst = Os + (warp * kRows + row) * LO + 16 * cc;
+      float* dst = Os + (grp * kRows + row) * LO + d0 + 16 * cc;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -272,20 +302,21 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
   __syncthreads();
   const int ranks = cluster > 1 ? cluster : 1;
   const bool split = cluster <= 1 && c.plan.n_slots > 1;
-  // Rows r, 64 dims a warp: the four warps' parts, in order, into the first one's place.
-  for (int p = warp; p < u.nrows * NI; p += kWarps) {
-    const int r = p / NI, d = 64 * (p - r * NI) + 2 * lane;
-    float2 ml[kWarps], x[kWarps];
+  // Rows r, 64 dims a warp: the groups' parts, in order, into the first one's place.
+  constexpr int ND = D / 64, NW = G * HV;
+  for (int p = warp; p < u.nrows * ND; p += NW) {
+    const int r = p / ND, d = 64 * (p - r * ND) + 2 * lane;
+    float2 ml[G], x[G];
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
+    for (int k = 0; k < G; ++k) {
       ml[k] = ML[k * kRows + r];
       x[k] = *reinterpret_cast<const float2*>(Os + (k * kRows + r) * LO + d);
       top = fmaxf(top, ml[k].x);
     }
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
+    for (int k = 0; k < G; ++k) {
       if (ml[k].x == -INFINITY) continue;
       const float w = exp2f(ml[k].x - top);
       sum += w * ml[k].y;
@@ -317,8 +348,8 @@ __global__ void __launch_bounds__(32 * kWarps, attention_decode_ctas(D))
   ptx::cluster_sync();
   const int rank = (int)ptx::cluster_ctarank();
   const uint32_t os_a = ptx::smem_u32(Os), j_a = ptx::smem_u32(Joined);
-  for (int p = rank * kWarps + warp; p < u.nrows * NI; p += ranks * kWarps) {
-    const int r = p / NI, d = 64 * (p - r * NI) + 2 * lane;
+  for (int p = rank * NW + warp; p < u.nrows * ND; p += ranks * NW) {
+    const int r = p / ND, d = 64 * (p - r * ND) + 2 * lane;
     float2 ml[8], x[8];
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -354,8 +385,8 @@ template <int D, bool F8>
 cudaError_t launch(const AttnCall& c, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)c.B * c.plan.tiles_e * c.plan.ne), c.Hkv);
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = decode_smem(D);
+  cfg.blockDim = dim3(Cfg<D, F8>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<D, F8>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -369,7 +400,7 @@ cudaError_t launch(const AttnCall& c, cudaStream_t st) {
 
 template <int D, bool F8>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_decode_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, decode_smem(D));
+  return cudaFuncSetAttribute(attn_decode_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, F8>::kSmem);
 }
 
 }  // namespace

@@ -492,7 +492,7 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   p.bm_e = p.decode ? kDecodeRows : c.bf16 ? most : p.rows_b <= 16 ? 16 : 64;
   p.bm_s = c.bf16 ? most : p.bm_e;
   p.kt_s = c.bf16 ? 128 : kKeys;
-  p.kt_e = p.decode ? kDecodeTile : p.kt_s;
+  p.kt_e = p.decode ? 16 * decode_groups(c.D) : p.kt_s;
   // Rows of several elements share a tile (and its pass over the prefix) when
   // one element's rows would leave half of it empty.
   const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : p.bm_e / 2);

@@ -78,8 +78,9 @@ int attention_tc_rows(int D);   // rows of a CTA
 // The few-row kernel (bf16 queries, 16 rows of an element or less).
 cudaError_t configure_attention_decode();
 cudaError_t launch_attention_decode(const AttnCall& c, cudaStream_t st);
-constexpr int kDecodeRows = 16, kDecodeTile = 64;
-constexpr int attention_decode_ctas(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }   // CTAs of an SM
+constexpr int kDecodeRows = 16;
+constexpr int decode_groups(int D) { return D == 256 ? 6 : 4; }                          // of 16 keys each, in a tile
+constexpr int attention_decode_ctas(int D) { return D == 256 ? 1 : D == 128 ? 3 : 4; }   // CTAs of an SM
 
 // One tensor of rows [outer][batch][token][head][D] for the cache kernels;
 // strides in elements, the outer index (keys, values, or layers of both)
