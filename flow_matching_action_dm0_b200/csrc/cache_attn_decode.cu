@@ -11,6 +11,12 @@
 //   O = P V      lane (n, c) takes 8 neighbouring dims of its four keys, and
 //                the eight of them are eight column tiles of its B fragment
 //                (an output column stands for another dim, undone on writing).
+// E4M3 codes become f16 (exactly, one conversion for two) and so do the
+// queries, each row times a power of two that brings its largest magnitude to
+// 2^14 (what is lost is below 2^-38 of it).  Their products with P are in
+// units of 2^mv, mv the running maximum of score + log2(value scale), so that
+// f16 weights hold what matters whatever the scales; the row's sum keeps the
+// maximum m of the scores alone, and O is brought to it at the end.
 // A group takes 16 keys of a tile with a running maximum of its own (raised,
 // and O rescaled, when it has grown by more than 8 in base 2); at head_dim
 // 256 it is two warps, each with half of the dims, that add their scores.
@@ -45,7 +51,7 @@ struct Cfg {
   static constexpr int kJoin = G * kRows * (LO + 2) * 4 + kRows * 8;
   static constexpr int kMain = kRing > kJoin ? kRing : kJoin;   // the join is staged over the ring
   static constexpr int kExchange = HV == 2 ? G * 2 * 32 * 32 : 0;   // scores of each half
-  static constexpr int kSmem = kRows * kQRow + kMain + kExchange;
+  static constexpr int kSmem = kRows * kQRow + kMain + kExchange + kRows * 4;   // and the queries' factors
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -53,14 +59,35 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 codes (low byte first) to two bf16 values, exactly (both fit in f16 and bf16).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  uint32_t h2;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(two));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  return ptx::pack_bf16x2(f.x, f.y);
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-
+// Four E4M3 codes (low byte first) to two pairs of f16, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// C[16x8] += A[16x16] * B[16x8], f16 in, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F8>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F8) mma_f16_16816(c, a, b0, b1);
+  else ptx::mma_bf16_16816(c, a, b0, b1);
+}
 // `bytes` of 16 (16-byte chunks) or 4 from global to shared memory; nothing is read, and zeros written, unless `on`.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -137,11 +164,36 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     *reinterpret_cast<uint4*>(Qs + r * C::kQRow + ch * 16) = v;
   }
   __syncthreads();
+  float qf[2] = {1.f, 1.f};                         // factors of rows n and n + 8
+  if (F8) {
+    float* factor = reinterpret_cast<float*>(sm + C::kSmem) - kRows;
+    for (int r = warp; r < kRows; r += G * HV) {
+      uint32_t* row = reinterpret_cast<uint32_t*>(Qs + r * C::kQRow);
+      uint32_t x[D / 64], top = 0u;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        x[i] = row[i * 32 + lane];
+        top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      // 2^(14 - exponent of the largest), and its inverse for the scores; 1 for a row of zeros or one that is not finite
+      const int e = top == 0u || top >= 0x7F80u ? 0 : min(max((int)(top >> 7) - 127 - 14, -126), 126);
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        row[i * 32 + lane] = pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xFFFF0000u) * f);
+      if (lane == 0) factor[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+    __syncthreads();
+    qf[0] = factor[n];
+    qf[1] = factor[n + 8];
+  }
 
   float o[NI * 8][4];
 #pragma unroll
   for (int j = 0; j < NI * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows n and n + 8
+  float mv[2] = {-INFINITY, -INFINITY};             // E4M3: O counts in units of 2^mv (bf16: of 2^m)
   const float scale = c.scale_log2;
   int slot = 0;
   for (int tile = u.t0; tile < u.t1; ++tile) {
@@ -170,16 +222,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
         const int k = n + 8 * h;
         if (F8) {
           const uint4 x = *reinterpret_cast<const uint4*>(stage + place(k, 4 * i + cc));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] = e4m3x2_to_bf16x2((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          e4m3x4_to_f16x4(x.x, b[0], b[1]);
+          e4m3x4_to_f16x4(x.y, b[2], b[3]);
+          e4m3x4_to_f16x4(x.z, b[4], b[5]);
+          e4m3x4_to_f16x4(x.w, b[6], b[7]);
         } else {
           const uint4 x = *reinterpret_cast<const uint4*>(stage + place(k, 8 * i + 2 * cc));
           const uint4 y = *reinterpret_cast<const uint4*>(stage + place(k, 8 * i + 2 * cc + 1));
           b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w, b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) ptx::mma_bf16_16816(s[h], a[t], b[2 * t], b[2 * t + 1]);
+        for (int t = 0; t < 4; ++t) mma<F8>(s[h], a[t], b[2 * t], b[2 * t + 1]);
       }
     }
     if (HV == 2) {   // the halves' scores, added in the same order by both
@@ -195,21 +248,27 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
       named_sync(1 + grp, 64);
     }
     // scores of rows n, n + 8 with keys 2c, 2c + 1 (+ 8 h)
-    float top[2] = {-INFINITY, -INFINITY};
+    float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
     const float* sc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes);
-    float2 vw[2];
+    float vw[4] = {1.f, 1.f, 1.f, 1.f}, lv[4] = {0.f, 0.f, 0.f, 0.f};   // value scales of keys 2c, 2c + 1, then + 8; their logarithms
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float2 kw = F8 ? *reinterpret_cast<const float2*>(sc + 8 * h + 2 * cc) : make_float2(1.f, 1.f);
-      vw[h] = F8 ? *reinterpret_cast<const float2*>(sc + 16 + 8 * h + 2 * cc) : make_float2(1.f, 1.f);
+      float2 kw = make_float2(1.f, 1.f);
+      if (F8) {
+        kw = *reinterpret_cast<const float2*>(sc + 8 * h + 2 * cc);
+        const float2 x = *reinterpret_cast<const float2*>(sc + 16 + 8 * h + 2 * cc);
+        vw[2 * h] = x.x, vw[2 * h + 1] = x.y;
+        lv[2 * h] = lg2(fabsf(x.x)), lv[2 * h + 1] = lg2(fabsf(x.y));   // (a hidden key's scale was filled with 0: -inf)
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const bool on = (bits >> (8 * h + 2 * cc + e)) & 1u;
         const float f = F8 ? (e ? kw.y : kw.x) * scale : scale;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          s[h][2 * r + e] = on ? s[h][2 * r + e] * f : -INFINITY;
+          s[h][2 * r + e] = on ? s[h][2 * r + e] * (F8 ? f * qf[r] : f) : -INFINITY;
           top[r] = fmaxf(top[r], s[h][2 * r + e]);
+          if (F8) topv[r] = fmaxf(topv[r], s[h][2 * r + e] + lv[2 * h + e]);
         }
       }
     }
@@ -218,14 +277,28 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     for (int r = 0; r < 2; ++r) {
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
       top[r] = fmaxf(m[r], fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)));
-      grow = grow || top[r] - m[r] > kLazy;         // (from -inf too)
+      if (F8) {
+        topv[r] = fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 1));
+        topv[r] = fmaxf(mv[r], fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 2)));
+        l[r] *= m[r] == top[r] ? 1.f : ex2(m[r] - top[r]);
+        m[r] = top[r];
+        grow = grow || topv[r] - mv[r] > kLazy;
+      } else {
+        grow = grow || top[r] - m[r] > kLazy;       // (from -inf too)
+      }
     }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float f = m[r] == top[r] ? 1.f : ex2(m[r] - top[r]);
-        m[r] = top[r];
-        l[r] *= f;
+        float f;
+        if (F8) {
+          f = mv[r] == topv[r] ? 1.f : ex2(mv[r] - topv[r]);
+          mv[r] = topv[r];
+        } else {
+          f = m[r] == top[r] ? 1.f : ex2(m[r] - top[r]);
+          m[r] = top[r];
+          l[r] *= f;
+        }
 #pragma unroll
         for (int j = 0; j < NI * 8; ++j) {
           o[j][2 * r] *= f;
@@ -238,40 +311,54 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
       float w[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float b = m[r] == -INFINITY ? 0.f : m[r];
+        const float b = m[r] == -INFINITY ? 0.f : m[r], bv = mv[r] == -INFINITY ? 0.f : mv[r];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float x = ex2(s[h][2 * r + e] - b);
             l[r] += x;
-            w[h][2 * r + e] = F8 ? x * (e ? vw[h].y : vw[h].x) : x;   // (a hidden key's scale was filled with 0)
+            w[h][2 * r + e] = F8 ? copysignf(ex2(s[h][2 * r + e] + lv[2 * h + e] - bv), vw[2 * h + e]) : x;
           }
       }
-      p[0] = ptx::pack_bf16x2(w[0][0], w[0][1]);
-      p[1] = ptx::pack_bf16x2(w[0][2], w[0][3]);
-      p[2] = ptx::pack_bf16x2(w[1][0], w[1][1]);
-      p[3] = ptx::pack_bf16x2(w[1][2], w[1][3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = w[k >> 1][2 * (k & 1)], b = w[k >> 1][2 * (k & 1) + 1];
+        p[k] = F8 ? pack_f16x2(a, b) : ptx::pack_bf16x2(a, b);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      uint32_t v[4][4];                             // keys 2c, 2c + 1, then + 8; dims 2w, 2w + 1 of 8
+      // keys k, k + 1 and k + 8, k + 9 (k = 2c); dims 2w, 2w + 1 of 8
+      const uint8_t* vt = stage + C::kTileBytes;
+      const int k = 2 * cc;
+      if (F8) {
+        uint2 x[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = 2 * cc + (q & 1) + 8 * (q >> 1);
-        if (F8) {
-          const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kTileBytes + place(k, 4 * i + (n >> 1)) + (n & 1) * 8);
-          v[q][0] = e4m3x2_to_bf16x2(x.x & 0xFFFFu), v[q][1] = e4m3x2_to_bf16x2(x.x >> 16);
-          v[q][2] = e4m3x2_to_bf16x2(x.y & 0xFFFFu), v[q][3] = e4m3x2_to_bf16x2(x.y >> 16);
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + C::kTileBytes + place(k, 8 * i + n));
+        for (int q = 0; q < 4; ++q)
+          x[q] = *reinterpret_cast<const uint2*>(vt + place(k + (q & 1) + 8 * (q >> 1), 4 * i + (n >> 1)) + (n & 1) * 8);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {               // the codes of two keys side by side, then to f16
+          const uint32_t a0 = w < 2 ? x[0].x : x[0].y, a1 = w < 2 ? x[1].x : x[1].y;
+          const uint32_t a2 = w < 2 ? x[2].x : x[2].y, a3 = w < 2 ? x[3].x : x[3].y;
+          uint32_t b0, b1, b2, b3;
+          e4m3x4_to_f16x4(__byte_perm(a0, a1, (w & 1) ? 0x7362 : 0x5140), b0, b1);
+          e4m3x4_to_f16x4(__byte_perm(a2, a3, (w & 1) ? 0x7362 : 0x5140), b2, b3);
+          mma<F8>(o[8 * i + 2 * w], p, b0, b2);
+          mma<F8>(o[8 * i + 2 * w + 1], p, b1, b3);
+        }
+      } else {
+        uint32_t v[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vt + place(k + (q & 1) + 8 * (q >> 1), 8 * i + n));
           v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
         }
-      }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        ptx::mma_bf16_16816(o[8 * i + 2 * w], p, __byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x5410));
-        ptx::mma_bf16_16816(o[8 * i + 2 * w + 1], p, __byte_perm(v[0][w], v[1][w], 0x7632), __byte_perm(v[2][w], v[3][w], 0x7632));
+        for (int w = 0; w < 4; ++w) {
+          mma<F8>(o[8 * i + 2 * w], p, __byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x5410));
+          mma<F8>(o[8 * i + 2 * w + 1], p, __byte_perm(v[0][w], v[1][w], 0x7632), __byte_perm(v[2][w], v[3][w], 0x7632));
+        }
       }
     }
   }
@@ -284,6 +371,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     const int row = n + 8 * r;
+    if (F8) {
+      const float f = mv[r] == m[r] ? 1.f : ex2(mv[r] - m[r]);
+#pragma unroll
+      for (int j = 0; j < NI * 8; ++j) {
+        o[j][2 * r] *= f;
+        o[j][2 * r + 1] *= f;
+      }
+    }
     // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
     if (cc == 0 && half == 0) ML[grp * kRows + row] = make_float2(l[r] != l[r] ? INFINITY : l[r] == 0.f ? -INFINITY : m[r], l[r]);
     if (row < u.nrows) {
