@@ -369,38 +369,37 @@ def _ocheck(h, s):
     return s
 
 
-def _ref(x):
-    return None if x is None else C.byref(x)
+def rtv_kv_write(h, src, cache, start_ptr, first: int, count_ptr, stream: int = 0):
+    s = _lib.rtv_kv_write(h, src, cache, start_ptr, first, count_ptr, stream)
+    return s if s == RTV_OK else _ocheck(h, s)
 
 
-def rtv_kv_write(h, src, cache, start_ptr: int, first: int, count_ptr: int, stream: int = 0):
-    return _ocheck(h, _lib.rtv_kv_write(h, _ref(src), _ref(cache), start_ptr, first, count_ptr, stream))
-
-
-def rtv_kv_read(h, cache, first: int, lens_ptr: int, dst, stream: int = 0):
-    return _ocheck(h, _lib.rtv_kv_read(h, _ref(cache), first, lens_ptr, _ref(dst), stream))
+def rtv_kv_read(h, cache, first: int, lens_ptr, dst, stream: int = 0):
+    s = _lib.rtv_kv_read(h, cache, first, lens_ptr, dst, stream)
+    return s if s == RTV_OK else _ocheck(h, s)
 
 
 def rtv_cross_attention(h, q, kv, lens_ptr, mask_ptr, mask_stride, workspace_ptr, workspace_bytes, stream: int = 0):
-    return _ocheck(h, _lib.rtv_cross_attention(h, _ref(q), _ref(kv), lens_ptr, mask_ptr, mask_stride, workspace_ptr,
-                                               workspace_bytes, stream))
+    s = _lib.rtv_cross_attention(h, q, kv, lens_ptr, mask_ptr, mask_stride, workspace_ptr, workspace_bytes, stream)
+    return s if s == RTV_OK else _ocheck(h, s)
 
 
 def rtv_cross_attention_workspace(h, q, kv) -> int:
     n = C.c_size_t(0)
-    _ocheck(h, _lib.rtv_cross_attention_workspace(h, _ref(q), _ref(kv), C.byref(n)))
+    _ocheck(h, _lib.rtv_cross_attention_workspace(h, q, kv, n))
     return n.value
 
 
 def rtv_shared_attention(h, q, prefix, prefix_mask_ptr, own, own_lens_ptr, workspace_ptr, workspace_bytes,
                          stream: int = 0):
-    return _ocheck(h, _lib.rtv_shared_attention(h, _ref(q), _ref(prefix), prefix_mask_ptr, _ref(own), own_lens_ptr,
-                                                workspace_ptr, workspace_bytes, stream))
+    s = _lib.rtv_shared_attention(h, q, prefix, prefix_mask_ptr, own, own_lens_ptr, workspace_ptr, workspace_bytes,
+                                  stream)
+    return s if s == RTV_OK else _ocheck(h, s)
 
 
 def rtv_shared_attention_workspace(h, q, prefix, own) -> int:
     n = C.c_size_t(0)
-    _ocheck(h, _lib.rtv_shared_attention_workspace(h, _ref(q), _ref(prefix), _ref(own), C.byref(n)))
+    _ocheck(h, _lib.rtv_shared_attention_workspace(h, q, prefix, own, n))
     return n.value
 
 
