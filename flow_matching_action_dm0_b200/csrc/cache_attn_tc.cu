@@ -507,24 +507,22 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       const uint32_t flip = c.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale becomes -q and its magnitude
       uint8_t* qt = Qs + (two ? grp * C::QB : 0);
       const int r0 = two ? 0 : 16 * grp, nr = two ? 32 : 16, ch = lane % CPR;
-#pragma unroll 1
-      for (int i = 0; i < nr; i += 8 * RPI) {
-        uint4 v[8];
+      uint4 v[32 / RPI < 16 ? 32 / RPI : 16];     // all of a group's rows at once (32 at head_dim 256 are never asked of one)
+      constexpr int NB = sizeof(v) / 16;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rl = r0 + i + k * RPI + lane / CPR;           // row of the warp's 32
-          const long long o = __shfl_sync(0xffffffffu, off, rl & 31);
-          v[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (i + k * RPI < nr && tile_row + 32 * quarter + rl < u.nrows)
-            v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + o + ch * 8);
-        }
+      for (int k = 0; k < NB; ++k) {
+        const int rl = r0 + k * RPI + lane / CPR;               // row of the warp's 32
+        const long long o = __shfl_sync(0xffffffffu, off, rl & 31);
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (k * RPI < nr && tile_row + 32 * quarter + rl < u.nrows)
+          v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + o + ch * 8);
+      }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rq = 32 * quarter + r0 + i + k * RPI + lane / CPR;
-          if (i + k * RPI >= nr) break;
-          v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
-          *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4)) = v[k];
-        }
+      for (int k = 0; k < NB; ++k) {
+        const int rq = 32 * quarter + r0 + k * RPI + lane / CPR;
+        if (k * RPI >= nr) continue;
+        v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+        *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4)) = v[k];
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();

@@ -32,10 +32,13 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // of 8 elements; the maximum over the row's magnitudes is taken on their bit
 // patterns, which order like the values with infinities and NaN on top.
 // ---------------------------------------------------------------------------
+constexpr int kRowsAhead = 4;                   // rows whose loads a thread has in flight
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_write_kernel(const CacheCall c) {
+__global__ void __launch_bounds__(256) kv_write_kernel(const __grid_constant__ CacheCall c) {
   constexpr int LPR = D / 8;                    // lanes of a row
-  constexpr int RPB = 256 / LPR;                // rows of a block
+  constexpr int RPB = 256 / LPR;                // rows of a block's step
+  constexpr int U = kRowsAhead;
   const int b = blockIdx.y, o = blockIdx.z;
   const int lane = threadIdx.x % LPR;
   int n = c.tokens;
@@ -45,63 +48,71 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const CacheCall c) {
     if (n != want && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
   }
   const long long at0 = (long long)c.first + (c.start ? c.start[b] : 0);
-  const long long rows = (long long)n * c.heads;
-  for (long long r0 = (long long)blockIdx.x * RPB; r0 < rows; r0 += (long long)gridDim.x * RPB) {
-    const long long r = r0 + threadIdx.x / LPR;
-    const int t = (int)(r / c.heads), h = (int)(r - (long long)t * c.heads);
-    const bool real = r < rows;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (real) {
-      const T* src = reinterpret_cast<const T*>(c.rows.base + o * c.rows.outer_bytes) + b * c.rows.sb + t * c.rows.st +
-                     h * c.rows.sh + lane * 8;
+  const unsigned rows = (unsigned)n * c.heads, step = gridDim.x * RPB * U;   // (tokens * heads < 2^30)
+  const char* src0 = c.rows.base + o * c.rows.outer_bytes + (b * c.rows.sb + lane * 8) * (long long)sizeof(T);
+  uint8_t* dst0 = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + lane * 8;
+  float* f0 = reinterpret_cast<float*>(reinterpret_cast<char*>(c.cache.scales) + o * c.cache.scales_outer) + b * c.cache.fb;
+  for (unsigned r0 = blockIdx.x * RPB * U; r0 < rows; r0 += step) {
+    uint4 v[U][sizeof(T) / 2];
+    unsigned t[U], h[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const unsigned r = r0 + k * RPB + threadIdx.x / LPR;
+      t[k] = r / (unsigned)c.heads;
+      h[k] = r - t[k] * c.heads;
+      const uint4* src = reinterpret_cast<const uint4*>(src0 + ((long long)t[k] * c.rows.st + h[k] * c.rows.sh) * (long long)sizeof(T));
+#pragma unroll
+      for (int w = 0; w < (int)sizeof(T) / 2; ++w) v[k][w] = r < rows ? __ldcs(src + w) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      float x[8];
       if (sizeof(T) == 2) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[2 * i] = __uint_as_float(w[i] << 16);
           x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
       } else {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(src)), w = __ldcs(reinterpret_cast<const float4*>(src) + 1);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+        constexpr int q = sizeof(T) / 2 - 1;
+        x[0] = __uint_as_float(v[k][0].x), x[1] = __uint_as_float(v[k][0].y), x[2] = __uint_as_float(v[k][0].z);
+        x[3] = __uint_as_float(v[k][0].w), x[4] = __uint_as_float(v[k][q].x), x[5] = __uint_as_float(v[k][q].y);
+        x[6] = __uint_as_float(v[k][q].z), x[7] = __uint_as_float(v[k][q].w);
       }
-    }
-    uint32_t top = 0;
+      uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
-    for (int k = LPR / 2; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
-    if (!real) continue;
-    const long long at = at0 + t;
-    if (at < 0 || at >= c.capacity) {
-      if (lane == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
-      continue;
-    }
-    // 448 = 1.75 * 2^8
-    const int e = max(-126, (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-    const bool finite = top < 0x7F800000u;
-    const float inv = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-    uint2 codes = make_uint2(0u, 0u);
-    if (finite) {
-      codes.x = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv) | f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
-      codes.y = f32x2_to_e4m3x2(x[4] * inv, x[5] * inv) | f32x2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
-    }
-    uint8_t* dst = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + at * c.cache.st + h * c.cache.sh;
-    *reinterpret_cast<uint2*>(dst + lane * 8) = codes;
-    if (lane == 0) {
-      float* f = reinterpret_cast<float*>(reinterpret_cast<char*>(c.cache.scales) + o * c.cache.scales_outer);
-      f[b * c.cache.fb + at * c.cache.ft + h * c.cache.fh] =
-          finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+      for (int i = LPR / 2; i > 0; i >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+      if (r0 + k * RPB + threadIdx.x / LPR >= rows) continue;
+      const long long at = at0 + t[k];
+      if (at < 0 || at >= c.capacity) {
+        if (lane == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
+        continue;
+      }
+      // 448 = 1.75 * 2^8
+      const int e = max(-126, (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+      const bool finite = top < 0x7F800000u;
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint2 codes = make_uint2(0u, 0u);
+      if (finite) {
+        codes.x = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv) | f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+        codes.y = f32x2_to_e4m3x2(x[4] * inv, x[5] * inv) | f32x2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+      }
+      *reinterpret_cast<uint2*>(dst0 + at * c.cache.st + h[k] * c.cache.sh) = codes;
+      if (lane == 0)
+        f0[at * c.cache.ft + h[k] * c.cache.fh] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
     }
   }
 }
 
 // Cache read: code * scale, rounded once.  A row is D/16 lanes of 16 codes.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(const CacheCall c) {
+__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ CacheCall c) {
   constexpr int LPR = D / 16;
   constexpr int RPB = 256 / LPR;
+  constexpr int U = kRowsAhead;
   const int b = blockIdx.y, o = blockIdx.z;
   const int lane = threadIdx.x % LPR;
   int n = c.capacity;   // valid cache tokens
@@ -110,39 +121,47 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const CacheCall c) {
     n = min(max(want, 0), c.capacity);
     if (n != want && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(c.status, RTV_DEV_BOUNDS);
   }
-  const long long rows = (long long)c.tokens * c.heads;
-  for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR; r < rows; r += (long long)gridDim.x * RPB) {
-    const int t = (int)(r / c.heads), h = (int)(r - (long long)t * c.heads);
-    const long long at = (long long)c.first + t;
-    float x[16];
+  const unsigned rows = (unsigned)c.tokens * c.heads, step = gridDim.x * RPB * U;   // (tokens * heads < 2^30)
+  const uint8_t* src0 = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + lane * 16;
+  const float* f0 = reinterpret_cast<const float*>(reinterpret_cast<const char*>(c.cache.scales) + o * c.cache.scales_outer) + b * c.cache.fb;
+  char* dst0 = c.rows.base + o * c.rows.outer_bytes + (b * c.rows.sb + lane * 16) * (long long)sizeof(T);
+  for (unsigned r0 = blockIdx.x * RPB * U; r0 < rows; r0 += step) {
+    uint4 v[U];
+    float s[U];
+    unsigned t[U], h[U];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (at < n) {
-      const uint8_t* src = c.cache.codes + o * c.cache.codes_outer + b * c.cache.sb + at * c.cache.st + h * c.cache.sh;
-      const float* f = reinterpret_cast<const float*>(reinterpret_cast<const char*>(c.cache.scales) + o * c.cache.scales_outer);
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
-      const float s = f[b * c.cache.fb + at * c.cache.ft + h * c.cache.fh];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int k = 0; k < U; ++k) {
+      const unsigned r = r0 + k * RPB + threadIdx.x / LPR;
+      t[k] = r / (unsigned)c.heads;
+      h[k] = r - t[k] * c.heads;
+      const long long at = (long long)c.first + t[k];
+      const bool real = r < rows && at < n;
+      v[k] = real ? __ldcs(reinterpret_cast<const uint4*>(src0 + at * c.cache.st + h[k] * c.cache.sh)) : make_uint4(0u, 0u, 0u, 0u);
+      s[k] = real ? f0[at * c.cache.ft + h[k] * c.cache.fh] : 1.f;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (r0 + k * RPB + threadIdx.x / LPR >= rows) continue;
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      float x[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 p = e4m3x2_to_f32x2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-        x[2 * i] = p.x * s;
-        x[2 * i + 1] = p.y * s;
+        x[2 * i] = p.x * s[k];
+        x[2 * i + 1] = p.y * s[k];
       }
-    }
-    T* dst = reinterpret_cast<T*>(c.rows.base + o * c.rows.outer_bytes) + b * c.rows.sb + t * c.rows.st +
-             h * c.rows.sh + lane * 16;
-    if (sizeof(T) == 2) {
-      uint4 u[2];
-      uint32_t* w = reinterpret_cast<uint32_t*>(u);
+      uint4* dst = reinterpret_cast<uint4*>(dst0 + ((long long)t[k] * c.rows.st + h[k] * c.rows.sh) * (long long)sizeof(T));
+      if (sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
-      reinterpret_cast<uint4*>(dst)[0] = u[0];
-      reinterpret_cast<uint4*>(dst)[1] = u[1];
-    } else {
+        for (int i = 0; i < 2; ++i)
+          __stcs(dst + i, make_uint4(ptx::pack_bf16x2(x[8 * i], x[8 * i + 1]), ptx::pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                                     ptx::pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), ptx::pack_bf16x2(x[8 * i + 6], x[8 * i + 7])));
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < 4; ++i)
+          __stcs(dst + i, make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                                     __float_as_uint(x[4 * i + 3])));
+      }
     }
   }
 }
@@ -215,6 +234,7 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
     __syncthreads();
     if (tid < kKeys) Ok[tid] = tid < nk && (!s.mask || s.mask[bb * s.mask_sb + k0 + tid]) ? 1.f : 0.f;
     __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < kKeys * C4; i += 256) {
       const int r = i / C4, d = (i - r * C4) * 4;
       float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
 // Join of a row's partial results: out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k.
 // `per` warps share a row, each taking every per-th slot with its loads in
 // flight together; their sums are added in warp order.  Empty parts (m = -inf)
-// are not read.
+// do not count.
 template <typename QT, int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnCall c, int per) {
   constexpr int V = D >= 128 ? 4 : 2, NC = D / (32 * V);   // elements of a lane's load, loads of a lane
@@ -359,9 +379,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     sum = warp_sum(sum);
 #pragma unroll 4
     for (int k = sub; k < n; k += per) {
-      const float mk = ml[k * rows].x;
-      if (mk == -INFINITY) continue;
-      const float w = exp2f(mk - top);
+      const float mk = ml[k * rows].x;            // (an empty part is loaded, whatever it holds, and not used)
+      const float w = mk == -INFINITY ? 0.f : exp2f(mk - top);
       const float* src = c.part_o + (base + k * rows) * D + lane * V;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
         if (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + 32 * V * i);
         else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src + 32 * V * i);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[i][e] = fmaf(w, v[e], acc[i][e]);
+        for (int e = 0; e < V; ++e) acc[i][e] = mk == -INFINITY ? acc[i][e] : fmaf(w, v[e], acc[i][e]);
       }
     }
   }
@@ -463,7 +482,7 @@ cudaError_t read_d(const CacheCall& c, const dim3& grid, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_write(const CacheCall& c, cudaStream_t st) {
-  const long long rpb = 2048 / c.dim, rows = (long long)c.tokens * c.heads;
+  const long long rpb = 2048 / c.dim * kRowsAhead, rows = (long long)c.tokens * c.heads;
   const dim3 grid((unsigned)std::min((rows + rpb - 1) / rpb, 65535LL), c.batch, c.outer);
   if (c.bf16) return c.dim == 64    ? write_d<__nv_bfloat16, 64>(c, grid, st)
                      : c.dim == 128 ? write_d<__nv_bfloat16, 128>(c, grid, st)
@@ -473,7 +492,7 @@ cudaError_t launch_kv_write(const CacheCall& c, cudaStream_t st) {
 }
 
 cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
-  const long long rpb = 4096 / c.dim, rows = (long long)c.tokens * c.heads;
+  const long long rpb = 4096 / c.dim * kRowsAhead, rows = (long long)c.tokens * c.heads;
   const dim3 grid((unsigned)std::min((rows + rpb - 1) / rpb, 65535LL), c.batch, c.outer);
   if (c.bf16) return c.dim == 64    ? read_d<__nv_bfloat16, 64>(c, grid, st)
                      : c.dim == 128 ? read_d<__nv_bfloat16, 128>(c, grid, st)

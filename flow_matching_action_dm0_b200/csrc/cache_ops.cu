@@ -87,6 +87,7 @@ rtv_status check_kv_shape(rtv_ops* h, const rtv_kv* a, const char* what) {
   if (a->batch < 0 || a->n_tokens < 0 || a->n_heads <= 0)
     return ofail(h, RTV_ERR_SHAPE, std::string(what) + ": bad sizes");
   if (a->batch > 65535 || a->n_heads > 65535) return ofail(h, RTV_ERR_SHAPE, std::string(what) + ": more than 65535 elements or heads");
+  if ((long long)a->n_tokens * a->n_heads >= 1LL << 30) return ofail(h, RTV_ERR_SHAPE, std::string(what) + ": 2^30 rows of an element or more");
   return check_dim(h, a->head_dim);
 }
 
