@@ -570,30 +570,42 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       ptx::tc_fence_after();
       const uint32_t s_tmem = tmem + grp * kTile + lanes;
       if (live) {
-        uint32_t x[4][32];
+        // A row of S is held in registers; beside E4M3's converters there are
+        // enough for half of one, which is read twice.
+        constexpr int XH = F8 ? 2 : 4;            // 32-column chunks held at once
+        uint32_t x[XH][32];
+        auto take = [&](int c0) {                 // scaled and masked scores of XH chunks
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld_32_async(s_tmem + 32 * cc, x[cc]);
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int cc = 0; cc < XH; ++cc) tmem_ld_32_async(s_tmem + 32 * (c0 + cc), x[cc]);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          tmem_wait_ld(x[cc]);
-          if (F8) {
+          for (int cc = 0; cc < XH; ++cc) {
+            tmem_wait_ld(x[cc]);
+            if (F8) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + 32 * cc + e);
-              x[cc][e] = __float_as_uint(__uint_as_float(x[cc][e]) * f.x);
-              x[cc][e + 1] = __float_as_uint(__uint_as_float(x[cc][e + 1]) * f.y);
-              x[cc][e + 2] = __float_as_uint(__uint_as_float(x[cc][e + 2]) * f.z);
-              x[cc][e + 3] = __float_as_uint(__uint_as_float(x[cc][e + 3]) * f.w);
+              for (int e = 0; e < 32; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + 32 * (c0 + cc) + e);
+                const float2 a = mul2(make_float2(__uint_as_float(x[cc][e]), __uint_as_float(x[cc][e + 1])), make_float2(f.x, f.y));
+                const float2 b = mul2(make_float2(__uint_as_float(x[cc][e + 2]), __uint_as_float(x[cc][e + 3])), make_float2(f.z, f.w));
+                x[cc][e] = __float_as_uint(a.x), x[cc][e + 1] = __float_as_uint(a.y);
+                x[cc][e + 2] = __float_as_uint(b.x), x[cc][e + 3] = __float_as_uint(b.y);
+              }
+            }
+            if (!whole) {
+              const uint32_t vis = seen[grp * 4 + c0 + cc];
+              if (vis != ~0u)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[cc][e] = (vis >> e) & 1u ? x[cc][e] : 0xFF800000u;
             }
           }
-          if (!whole) {
-            const uint32_t vis = seen[grp * 4 + cc];
+        };
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[cc][e] = (vis >> e) & 1u ? x[cc][e] : 0xFF800000u;
-          }
+        for (int c0 = 0; c0 < 4; c0 += XH) {
+          take(c0);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[cc][e]));
+          for (int cc = 0; cc < XH; ++cc)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[cc][e]));
         }
         const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         float before = m;
@@ -636,28 +648,32 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t w[16];
+        for (int c0 = 0; c0 < 4; c0 += XH) {
+          if (F8) take(c0);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float2 p[2];
+          for (int cc = 0; cc < XH; ++cc) {
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 y = make_float2(__uint_as_float(x[cc][e + 2 * k]), __uint_as_float(x[cc][e + 2 * k + 1]));
-              p[k] = F8 ? add2(y, base2) : fma2(y, scale2, base2);
-              p[k].x = ex2(p[k].x);
-              p[k].y = ex2(p[k].y);
-              l2[k] = add2(l2[k], p[k]);
+            for (int e = 0; e < 32; e += 4) {
+              float2 p[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 y = make_float2(__uint_as_float(x[cc][e + 2 * k]), __uint_as_float(x[cc][e + 2 * k + 1]));
+                p[k] = F8 ? add2(y, base2) : fma2(y, scale2, base2);
+                p[k].x = ex2(p[k].x);
+                p[k].y = ex2(p[k].y);
+                l2[k] = add2(l2[k], p[k]);
+              }
+              if (F8) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + 128 + 32 * (c0 + cc) + e);
+                p[0] = mul2(p[0], make_float2(f.x, f.y));
+                p[1] = mul2(p[1], make_float2(f.z, f.w));
+              }
+              w[e / 2] = ptx::pack_bf16x2(p[0].x, p[0].y);
+              w[e / 2 + 1] = ptx::pack_bf16x2(p[1].x, p[1].y);
             }
-            if (F8) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + 128 + 32 * cc + e);
-              p[0] = mul2(p[0], make_float2(f.x, f.y));
-              p[1] = mul2(p[1], make_float2(f.z, f.w));
-            }
-            w[e / 2] = ptx::pack_bf16x2(p[0].x, p[0].y);
-            w[e / 2 + 1] = ptx::pack_bf16x2(p[1].x, p[1].y);
+            tmem_st_16(s_tmem + 16 * (c0 + cc), w);   // over S columns that have been read
           }
-          tmem_st_16(s_tmem + 16 * cc, w);
         }
         l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         tmem_wait_st();
@@ -665,11 +681,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       if (!whole && !(two && grp)) {
         // hidden values become zeros: their weight is 0, and 0 times anything stored there must be 0
         wait(&v_landed[grp], partial++);
-        if (!((seen[grp * 4 + quarter] >> lane) & 1u)) {
-          uint8_t* dst = ring + ((order.of_v(j) * NC + r / VK) % NST) * kStage + (r % VK) * 128;
+        const uint32_t hidden = ~seen[grp * 4 + quarter];
+        if (hidden) {                             // (the same in the warp's lanes: 8 of them write a key's 128 bytes)
+          const int cnt = order.of_v(j) * NC;
 #pragma unroll 1
-          for (int k = 0; k < NC * 8; ++k)
-            *reinterpret_cast<uint4*>(dst + (k >> 3) * VK * 128 + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          for (int k = lane >> 3; k < 32; k += 4) {
+            if (!((hidden >> k) & 1u)) continue;
+            const int key = 32 * quarter + k;
+            uint8_t* dst = ring + ((cnt + key / VK) % NST) * kStage + (key % VK) * 128 + (lane & 7) * 16;
+#pragma unroll
+            for (int dc = 0; dc < NC; ++dc) *reinterpret_cast<uint4*>(dst + dc * VK * 128) = make_uint4(0u, 0u, 0u, 0u);
+          }
           ptx::fence_proxy_async_smem();
         }
       }
