@@ -179,12 +179,15 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// Two E4M3 codes (low byte first) to two bf16 values, exactly (both fit in f16 and bf16).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  uint32_t h2;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(two));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  return ptx::pack_bf16x2(f.x, f.y);
+// Four E4M3 codes (low byte first) to two pairs of bf16, exactly (f16 and bf16 hold every E4M3 value).
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = ptx::pack_bf16x2(x.x, x.y);
+  hi = ptx::pack_bf16x2(y.x, y.y);
 }
 
 // The order of a unit's loads is that of their first use: with two row tiles
@@ -462,22 +465,23 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         used ^= 1u;
         wait(&empty[s], use + 1);
         ++use;
-        const int c16 = lane & 3;
+        const int c16 = lane & 3;                 // 16 codes of row 8 k + lane / 4 at a time: rows of one residue mod 8
+        uint8_t* d0 = dst + (lane >> 2) * 128 + (((2 * c16) ^ (lane >> 2)) << 4);
+        uint8_t* d1 = dst + (lane >> 2) * 128 + (((2 * c16 + 1) ^ (lane >> 2)) << 4);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint4 v[8];
+        for (int h = 0; h < 16; h += 4) {
+          uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (h * 8 + k) * 512);
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (h + k) * 512);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int row = (h * 8 + k) * 8 + (lane >> 2);
+          for (int k = 0; k < 4; ++k) {
             uint4 a, b;
-            a.x = e4m3x2_to_bf16x2(v[k].x & 0xFFFFu), a.y = e4m3x2_to_bf16x2(v[k].x >> 16);
-            a.z = e4m3x2_to_bf16x2(v[k].y & 0xFFFFu), a.w = e4m3x2_to_bf16x2(v[k].y >> 16);
-            b.x = e4m3x2_to_bf16x2(v[k].z & 0xFFFFu), b.y = e4m3x2_to_bf16x2(v[k].z >> 16);
-            b.z = e4m3x2_to_bf16x2(v[k].w & 0xFFFFu), b.w = e4m3x2_to_bf16x2(v[k].w >> 16);
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((2 * c16) ^ (row & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((2 * c16 + 1) ^ (row & 7)) << 4)) = b;
+            e4m3x4_to_bf16x4(v[k].x, a.x, a.y);
+            e4m3x4_to_bf16x4(v[k].y, a.z, a.w);
+            e4m3x4_to_bf16x4(v[k].z, b.x, b.y);
+            e4m3x4_to_bf16x4(v[k].w, b.z, b.w);
+            *reinterpret_cast<uint4*>(d0 + (h + k) * 1024) = a;
+            *reinterpret_cast<uint4*>(d1 + (h + k) * 1024) = b;
           }
         }
         ptx::fence_proxy_async_smem();
