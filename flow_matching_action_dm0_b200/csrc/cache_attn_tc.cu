@@ -1,6 +1,6 @@
 // bf16 attention over key/value caches on the tensor cores: one kernel for
 // cross attention, for a prefix shared by a batch and for each element's own
-// keys, bf16 or E4M3.
+// keys.
 //
 // A CTA takes up to 256 rows (query token x head of a KV head's group; 128 at
 // head_dim 256) against a range of 128-key tiles, in one pass over them:
@@ -21,8 +21,7 @@
 // with fewer, key tile q for the one row tile, the groups handing its maximum
 // on.  The MMA warp issues S(q + 1) before PV(q), so that the tensor cores
 // have work while a group exponentiates.  Warp 0 issues the loads, warp 1 the
-// MMAs; with an E4M3 source six warps widen codes to bf16 stages (exactly),
-// and the scales multiply S and P in fp32.
+// MMAs, warps 4-11 are the groups.
 #include <cuda.h>
 
 #include <algorithm>
@@ -36,7 +35,6 @@ namespace rtv {
 namespace {
 
 constexpr int kStage = 16384;                    // a bf16 stage: 128 rows of 128 bytes
-constexpr int kRaw = 8192;                       // the E4M3 codes of a stage: 128 rows of 64 bytes
 constexpr int kTile = 128;                       // rows of a unit, keys of a tile
 constexpr float kLazy = 8.f;                     // growth of a maximum (base 2) that rescales O
 constexpr long long kDrainNs = 200000000LL;      // limit of the waits for what is in flight after a timeout
@@ -48,24 +46,25 @@ struct __align__(64) AttnMaps {
   int pre_h, own_b, own_h;
 };
 
-template <int D, bool F8>
+template <int D>
 struct Cfg {
   static constexpr int NC = D / 64;                       // stages of a K or V tile
   static constexpr int VK = 8192 / D;                     // keys of a V stage
   static constexpr int MT = D == 256 ? 1 : 2;             // row tiles that fit the tensor memory
   static constexpr int QB = kTile * D * 2;                // bytes of a Q tile
-  static constexpr int NST = F8 ? 6 : 10;
-  static constexpr int kThreads = F8 ? 512 : 384;
+  static constexpr int NST = 10;
+  static constexpr int kThreads = 384;
   static constexpr int kSoft = 4;                         // first softmax warp
   // Registers of a softmax thread (it holds a row of S) and of the others:
-  // 8 warps of the one and 4 (8) of the other use what the CTA was launched with.
-  static constexpr int kLaunchRegs = F8 ? 128 : 168, kSoftRegs = F8 ? 168 : 208, kOtherRegs = 88;
+  // together what the CTA was launched with.
+  static constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
   static_assert(256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "register shares");
-  static constexpr int kOff = MT * QB + NST * kStage + (F8 ? NST * kRaw : 0);   // barriers behind the tiles
-  static constexpr int kSmall = 512 + 512 + 4 * 128 + (F8 ? 4 * 2 * kTile * 4 : 0);   // barriers, exchange, scales
+  static constexpr int kOff = MT * QB + NST * kStage;     // barriers behind the tiles
+  static constexpr int kSmall = 512 + 512 + 64;           // barriers, maxima, visible keys
   static constexpr int kSmem = 1024 + kOff + kSmall;
   static constexpr int kRowBytes = D * 4 + 16;            // a staged output row
   static_assert(MT * kTile * kRowBytes <= kOff, "output rows are staged where the tiles were");
+  static_assert(2 * NC <= NST, "V(j) and the next K are held at once");
   static_assert(kSmem <= 232448 - 64, "shared memory of a CTA");
 };
 
@@ -163,13 +162,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -179,17 +171,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// Four E4M3 codes (low byte first) to two pairs of bf16, exactly (f16 and bf16 hold every E4M3 value).
-__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  uint32_t a, b;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  lo = ptx::pack_bf16x2(x.x, x.y);
-  hi = ptx::pack_bf16x2(y.x, y.y);
-}
-
 // The order of a unit's loads is that of their first use: with two row tiles
 // K(0), V(0), K(1), V(1), ...; with one, S runs a key tile ahead:
 // K(0), K(1), V(0), K(2), V(1), ...
@@ -234,31 +215,27 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
                : "memory");
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attn_cache_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnMaps maps) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D>;
   constexpr int NC = C::NC, NST = C::NST, VK = C::VK;
   extern __shared__ uint8_t sm_raw[];
   __shared__ int s_abort;
   uint8_t* Qs = (uint8_t*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = Qs + C::MT * C::QB;
-  uint8_t* raw = ring + NST * kStage;             // E4M3: the codes of each stage
   uint64_t* ready = (uint64_t*)(Qs + C::kOff);    // [NST] the stage holds its operand
   uint64_t* empty = ready + NST;                  // [NST] the stage's MMAs have completed
-  uint64_t* raw_full = empty + NST;               // [NST] E4M3
-  uint64_t* raw_empty = raw_full + NST;           // [NST]
-  uint64_t* s_full = raw_empty + NST;             // [2] S of a buffer is complete
+  uint64_t* s_full = empty + NST;                 // [2] S of a buffer is complete
   uint64_t* p_ready = s_full + 2;                 // [2] P of a buffer is written (and hidden values are zeroed)
   uint64_t* v_landed = p_ready + 2;               // [2] the values of a step with hidden keys are in their stages
   uint64_t* q_ready = v_landed + 2;               // [2] Q rows of a group
   uint64_t* pv_done = q_ready + 2;                // one row tile: O += P V of a step has completed
   uint64_t* o_done = pv_done + 1;                 // every MMA of the CTA has completed
   uint32_t* tslot = (uint32_t*)(o_done + 1);
-  static_assert((4 * NST + 10) * 8 + 8 <= 512, "barriers fit their space");
+  static_assert((2 * NST + 10) * 8 + 8 <= 512, "barriers fit their space");
   float* m_row = (float*)(Qs + C::kOff + 512);    // [128] the maximum that the groups hand on (one row tile)
   uint32_t* seen = (uint32_t*)(m_row + 128);      // [2 groups][4] visible keys of the group's tile
-  float* scales = m_row + 256;                    // E4M3: [2 groups][2][K, V][128]
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform)
@@ -267,10 +244,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     for (int i = 0; i < NST; ++i) {
       ptx::mbar_init(&ready[i], 1);
       ptx::mbar_init(&empty[i], 1);
-      if (F8) {
-        ptx::mbar_init(&raw_full[i], 1);
-        ptx::mbar_init(&raw_empty[i], 1);
-      }
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s_full[i], 1);
@@ -313,42 +286,27 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     return false;
   };
   // One load of the order: the boxes of a stage, K chunk or V keys.
-  auto load = [&](int o, int cc, uint8_t* dst, uint64_t* bar, int row) {
+  auto load = [&](int o, int cc, uint8_t* dst, uint64_t* bar) {
     const TileAt t = tile_at(u, u.t0 + (o >> 1));
     const CUtensorMap* map = t.pre ? ((o & 1) ? &maps.pre_v : &maps.pre_k) : ((o & 1) ? &maps.own_v : &maps.own_k);
     const int h = u.kvh * (t.pre ? maps.pre_h : maps.own_h), b = t.pre ? 0 : u.b * maps.own_b;
-    ptx::mbar_expect_tx(bar, 128u * row);
+    ptx::mbar_expect_tx(bar, (uint32_t)kStage);
     if (!(o & 1)) {
       tma_load_4d(dst, map, 64 * cc, t.k0, h, b, bar);
     } else {
 #pragma unroll
-      for (int dc = 0; dc < NC; ++dc) tma_load_4d(dst + dc * VK * row, map, 64 * dc, t.k0 + cc * VK, h, b, bar);
+      for (int dc = 0; dc < NC; ++dc) tma_load_4d(dst + dc * VK * 128, map, 64 * dc, t.k0 + cc * VK, h, b, bar);
     }
   };
-  auto is_codes = [&](int o) { return F8 && (tile_at(u, u.t0 + (o >> 1)).pre ? c.pre_f8 : c.own_f8); };
-
   if (warp == 0) {
-    // ---- loads: bf16 into the stages, or codes into the stages' raw slots ----
+    // ---- loads ---------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
-      int st = 0;
-      uint32_t used = 0;                          // parity of each raw slot's uses
       bool ok = true;
-      for (int i = 0; i < 2 * n && ok; ++i) {
-        const int o = order.at(i);
-        const bool codes = is_codes(o);
-        for (int cc = 0; cc < NC && ok; ++cc, ++st) {
-          const int s = st % NST;
-          if (F8) {
-            if (!codes) continue;                 // its stage's warp loads it
-            if (!(ok = wait(&raw_empty[s], (int)(used >> s) + 1))) break;
-            used ^= 1u << s;
-            load(o, cc, raw + s * kRaw, &raw_full[s], 64);
-          } else {
-            if (!(ok = wait(&empty[s], st / NST + 1))) break;
-            load(o, cc, ring + s * kStage, &ready[s], 128);
-          }
-        }
+      for (int i = 0; i < 2 * n * NC && ok; ++i) {
+        const int s = i % NST;
+        ok = wait(&empty[s], i / NST + 1);
+        if (ok) load(order.at(i / NC), i % NC, ring + s * kStage, &ready[s]);
       }
     }
     __syncwarp();
@@ -402,8 +360,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         ptx::tc_fence_after();
         scores(1);
       }
-      // What the ring holds at once: V(j) and the next K, unless it is small.
-      constexpr bool kAhead = 2 * NC <= NST;
       for (int q = 0; q < steps && ok; ++q) {
         const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
         if (rt == 0) {
@@ -411,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if (((j < own0 ? pre_mask : own_mask) || j == pre_end || j == own_end) && leader && ok) ptx::mbar_arrive(&v_landed[buf]);
         }
         const bool next = q + 2 < steps;
-        if (kAhead && next && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
+        if (next && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
         ok = ok && wait(&p_ready[buf], q >> 1);
         ptx::tc_fence_after();
         int s = (order.of_v(j) * NC) % NST;
@@ -429,8 +385,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if (!two) ptx::umma_commit(pv_done);
         }
         if (next) {
-          if (!kAhead && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
-          ptx::tc_fence_after();
           scores(q + 2);
         }
       }
@@ -441,57 +395,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < C::kSoft || warp >= C::kSoft + 8) {
-    // ---- E4M3 codes to bf16 stages: a warp per stage of the ring -------------
-    // (every use of a stage is its warp's, so the phases it waits for follow
-    // one another: a parity tells a phase only from its neighbours)
+  } else if (warp < C::kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (F8) {
-      const int s = warp < 4 ? warp - 2 : warp - 10;   // warps 2, 3, 12..15
-      uint8_t* dst = ring + s * kStage;
-      const uint8_t* src = raw + s * kRaw + lane * 16;
-      uint32_t used = 0;
-      int use = 0;                                // uses of the stage so far
-      for (int i = 0; i < 2 * n * NC; ++i) {
-        if (i % NST != s) continue;
-        const int o = order.at(i / NC), cc = i % NC;
-        if (!is_codes(o)) {
-          if (wait(&empty[s], use + 1) && lane == 0) load(o, cc, dst, &ready[s], 128);
-          __syncwarp();
-          ++use;
-          continue;
-        }
-        wait(&raw_full[s], used);
-        used ^= 1u;
-        wait(&empty[s], use + 1);
-        ++use;
-        const int c16 = lane & 3;                 // 16 codes of row 8 k + lane / 4 at a time: rows of one residue mod 8
-        uint8_t* d0 = dst + (lane >> 2) * 128 + (((2 * c16) ^ (lane >> 2)) << 4);
-        uint8_t* d1 = dst + (lane >> 2) * 128 + (((2 * c16 + 1) ^ (lane >> 2)) << 4);
-#pragma unroll 1
-        for (int h = 0; h < 16; h += 4) {
-          uint4 v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (h + k) * 512);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 a, b;
-            e4m3x4_to_bf16x4(v[k].x, a.x, a.y);
-            e4m3x4_to_bf16x4(v[k].y, a.z, a.w);
-            e4m3x4_to_bf16x4(v[k].z, b.x, b.y);
-            e4m3x4_to_bf16x4(v[k].w, b.z, b.w);
-            *reinterpret_cast<uint4*>(d0 + (h + k) * 1024) = a;
-            *reinterpret_cast<uint4*>(d1 + (h + k) * 1024) = b;
-          }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&ready[s]);
-          ptx::mbar_arrive(&raw_empty[s]);
-        }
-      }
-    }
   } else {
     // ---- softmax: a row a thread ----------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
@@ -535,81 +440,44 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const float scale = fabsf(c.scale_log2);
     float m = -INFINITY, l = 0.f;                 // l counts in units of 2^m
     int partial = 0;                              // steps with hidden keys so far
-    // E4M3: the scales of key r of the group's next tile are fetched a step ahead
-    float ks = 1.f, vs = 1.f;
-    auto fetch = [&](int q) {
-      if (!F8 || q >= steps) return;
-      const TileAt a = tile_at(u, u.t0 + (two ? q >> 1 : q));
-      ks = vs = 1.f;
-      if (!(a.pre ? c.pre_f8 : c.own_f8) || r >= a.nk) return;
-      const long long fb = a.pre ? 0 : u.b * c.own.fb;
-      const long long off = fb + (long long)(a.k0 + r) * (a.pre ? c.pre.ft : c.own.ft) + u.kvh * (a.pre ? c.pre.fh : c.own.fh);
-      ks = (a.pre ? c.pre.ks : c.own.ks)[off];
-      vs = (a.pre ? c.pre.vs : c.own.vs)[off];
+    // Whether key r of the tile of step q is seen; looked up a step ahead.
+    auto sees = [&](int q) {
+      if (q >= steps) return false;
+      const TileAt t = tile_at(u, u.t0 + (two ? q >> 1 : q));
+      const uint8_t* mask = t.pre ? c.pre.mask : c.own.mask;
+      return r < t.nk && (!mask || mask[(t.pre ? 0 : u.b * c.own.mask_sb) + t.k0 + r]);
     };
-    fetch(grp);
+    bool next_vis = sees(grp);
     for (int q = grp; q < steps; q += 2) {
       const int j = two ? q >> 1 : q;
       const TileAt t = tile_at(u, u.t0 + j);
       const bool whole = !has_hidden(c, t);
-      float* sc = scales + (grp * 2 + ((q >> 1) & 1)) * 256;
-      if (!whole || F8) {
-        bool vis = true;
-        if (!whole) {
-          const uint8_t* mask = t.pre ? c.pre.mask : c.own.mask;
-          vis = r < t.nk && (!mask || mask[(t.pre ? 0 : u.b * c.own.mask_sb) + t.k0 + r]);
-          const uint32_t word = __ballot_sync(0xffffffffu, vis);
-          // (the group's last look at the words of its previous step was before its P was complete)
-          named_sync(2 + grp, 128);
-          if (lane == 0) seen[grp * 4 + quarter] = word;
-        }
-        if (F8) {
-          sc[r] = vis ? ks * scale : 1.f;         // the scale of the scores goes with the key's
-          sc[128 + r] = vis ? vs : 0.f;
-          fetch(q + 2);
-        }
+      if (!whole) {
+        const uint32_t word = __ballot_sync(0xffffffffu, next_vis);
+        // (the group's last look at the words of its previous step was before its P was complete)
+        named_sync(2 + grp, 128);
+        if (lane == 0) seen[grp * 4 + quarter] = word;
         named_sync(2 + grp, 128);
       }
+      next_vis = sees(q + 2);
       wait(&s_full[grp], q >> 1);
       ptx::tc_fence_after();
       const uint32_t s_tmem = tmem + grp * kTile + lanes;
       if (live) {
-        // A row of S is held in registers; beside E4M3's converters there are
-        // enough for half of one, which is read twice.
-        constexpr int XH = F8 ? 2 : 4;            // 32-column chunks held at once
-        uint32_t x[XH][32];
-        auto take = [&](int c0) {                 // scaled and masked scores of XH chunks
+        uint32_t x[4][32];                        // the row of S
 #pragma unroll
-          for (int cc = 0; cc < XH; ++cc) tmem_ld_32_async(s_tmem + 32 * (c0 + cc), x[cc]);
-#pragma unroll
-          for (int cc = 0; cc < XH; ++cc) {
-            tmem_wait_ld(x[cc]);
-            if (F8) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(sc + 32 * (c0 + cc) + e);
-                const float2 a = mul2(make_float2(__uint_as_float(x[cc][e]), __uint_as_float(x[cc][e + 1])), make_float2(f.x, f.y));
-                const float2 b = mul2(make_float2(__uint_as_float(x[cc][e + 2]), __uint_as_float(x[cc][e + 3])), make_float2(f.z, f.w));
-                x[cc][e] = __float_as_uint(a.x), x[cc][e + 1] = __float_as_uint(a.y);
-                x[cc][e + 2] = __float_as_uint(b.x), x[cc][e + 3] = __float_as_uint(b.y);
-              }
-            }
-            if (!whole) {
-              const uint32_t vis = seen[grp * 4 + c0 + cc];
-              if (vis != ~0u)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[cc][e] = (vis >> e) & 1u ? x[cc][e] : 0xFF800000u;
-            }
-          }
-        };
+        for (int cc = 0; cc < 4; ++cc) tmem_ld_32_async(s_tmem + 32 * cc, x[cc]);
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c0 = 0; c0 < 4; c0 += XH) {
-          take(c0);
+        for (int cc = 0; cc < 4; ++cc) {
+          tmem_wait_ld(x[cc]);
+          if (!whole) {
+            const uint32_t vis = seen[grp * 4 + cc];
 #pragma unroll
-          for (int cc = 0; cc < XH; ++cc)
+            for (int e = 0; e < 32; ++e) x[cc][e] = (vis >> e) & 1u ? x[cc][e] : 0xFF800000u;
+          }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[cc][e]));
+          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[cc][e]));
         }
         const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         float before = m;
@@ -617,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if (q > 0) named_sync(4 + 2 * quarter + grp, 64);
           before = q > 0 ? m_row[r] : -INFINITY;
         }
-        const float mn = fmaxf(before, F8 ? top : top * scale);
+        const float mn = fmaxf(before, top * scale);
         float now = before;
         if (j == 0) {
           now = mn;
@@ -652,32 +520,22 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
-        for (int c0 = 0; c0 < 4; c0 += XH) {
-          if (F8) take(c0);
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t w[16];
 #pragma unroll
-          for (int cc = 0; cc < XH; ++cc) {
-            uint32_t w[16];
+          for (int e = 0; e < 32; e += 4) {
+            float2 p[2];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float2 p[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float2 y = make_float2(__uint_as_float(x[cc][e + 2 * k]), __uint_as_float(x[cc][e + 2 * k + 1]));
-                p[k] = F8 ? add2(y, base2) : fma2(y, scale2, base2);
-                p[k].x = ex2(p[k].x);
-                p[k].y = ex2(p[k].y);
-                l2[k] = add2(l2[k], p[k]);
-              }
-              if (F8) {
-                const float4 f = *reinterpret_cast<const float4*>(sc + 128 + 32 * (c0 + cc) + e);
-                p[0] = mul2(p[0], make_float2(f.x, f.y));
-                p[1] = mul2(p[1], make_float2(f.z, f.w));
-              }
-              w[e / 2] = ptx::pack_bf16x2(p[0].x, p[0].y);
-              w[e / 2 + 1] = ptx::pack_bf16x2(p[1].x, p[1].y);
+            for (int k = 0; k < 2; ++k) {
+              p[k] = fma2(make_float2(__uint_as_float(x[cc][e + 2 * k]), __uint_as_float(x[cc][e + 2 * k + 1])), scale2, base2);
+              p[k].x = ex2(p[k].x);
+              p[k].y = ex2(p[k].y);
+              l2[k] = add2(l2[k], p[k]);
             }
-            tmem_st_16(s_tmem + 16 * (c0 + cc), w);   // over S columns that have been read
+            w[e / 2] = ptx::pack_bf16x2(p[0].x, p[0].y);
+            w[e / 2 + 1] = ptx::pack_bf16x2(p[1].x, p[1].y);
           }
+          tmem_st_16(s_tmem + 16 * cc, w);        // over S columns that have been read
         }
         l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         tmem_wait_st();
@@ -800,69 +658,60 @@ EncodeFn encode_fn() {
 }
 
 // Map of one tensor [batch][token][head][D] with boxes of 64 dims x `keys` tokens.
-bool encode(CUtensorMap* m, const void* base, bool f8, int D, int keys, int len, int heads, long long st, long long sh,
-            int batch, long long sb) {
-  const long long eb = f8 ? 1 : 2, dense = (long long)D * eb;
+bool encode(CUtensorMap* m, const void* base, int D, int keys, int len, int heads, long long st, long long sh, int batch,
+            long long sb) {
+  const long long dense = 2LL * D;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)len, (cuuint64_t)heads, (cuuint64_t)batch};
-  const cuuint64_t strides[3] = {(cuuint64_t)(len > 1 ? st * eb : dense), (cuuint64_t)(heads > 1 ? sh * eb : dense),
-                                 (cuuint64_t)(batch > 1 ? sb * eb : dense)};
+  const cuuint64_t strides[3] = {(cuuint64_t)(len > 1 ? 2 * st : dense), (cuuint64_t)(heads > 1 ? 2 * sh : dense),
+                                 (cuuint64_t)(batch > 1 ? 2 * sb : dense)};
   const cuuint32_t box[4] = {64, (cuuint32_t)keys, 1, 1}, one[4] = {1, 1, 1, 1};
-  return encode_fn()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
-                     dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool F8>
+template <int D>
 cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D>;
   AttnMaps m{};
   bool ok = true;
-  auto source = [&](const KvSource& s, int f8, int batch, CUtensorMap* k, CUtensorMap* v, int* hm, int* bm) {
+  auto source = [&](const KvSource& s, int batch, CUtensorMap* k, CUtensorMap* v, int* hm, int* bm) {
     if (s.len == 0) return;
     *hm = c.Hkv > 1 && s.sh == 0 ? 0 : 1;
     *bm = batch > 1 && s.sb == 0 ? 0 : 1;
     const int heads = *hm ? c.Hkv : 1, nb = *bm ? batch : 1;
-    ok = ok && encode(k, s.k, f8, D, kTile, s.len, heads, s.st, s.sh, nb, s.sb) &&
-         encode(v, s.v, f8, D, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
+    ok = ok && encode(k, s.k, D, kTile, s.len, heads, s.st, s.sh, nb, s.sb) &&
+         encode(v, s.v, D, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
   };
   int pre_b = 0;
-  source(c.pre, c.pre_f8, 1, &m.pre_k, &m.pre_v, &m.pre_h, &pre_b);
-  if (!c.plan.decode) source(c.own, c.own_f8, c.B, &m.own_k, &m.own_v, &m.own_h, &m.own_b);
+  source(c.pre, 1, &m.pre_k, &m.pre_v, &m.pre_h, &pre_b);
+  if (!c.plan.decode) source(c.own, c.B, &m.own_k, &m.own_v, &m.own_h, &m.own_b);
   if (!ok) return cudaErrorInvalidValue;
   const long long elems = c.plan.decode ? 0 : (long long)c.B * c.plan.tiles_e * c.plan.ne;
   const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + elems), c.Hkv);
-  attn_cache_kernel<D, F8><<<grid, C::kThreads, C::kSmem, st>>>(c, m);
+  attn_cache_kernel<D><<<grid, C::kThreads, C::kSmem, st>>>(c, m);
   return cudaGetLastError();
 }
 
-template <int D, bool F8>
+template <int D>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_cache_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, F8>::kSmem);
+  return cudaFuncSetAttribute(attn_cache_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
 }
 
 }  // namespace
 
 cudaError_t configure_attention_tc() {
   if (!encode_fn()) return cudaErrorNotSupported;
-  cudaError_t e = cudaSuccess;
-  auto chain = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-  chain(configure<64, false>());
-  chain(configure<128, false>());
-  chain(configure<256, false>());
-  chain(configure<64, true>());
-  chain(configure<128, true>());
-  chain(configure<256, true>());
+  cudaError_t e = configure<64>();
+  if (e == cudaSuccess) e = configure<128>();
+  if (e == cudaSuccess) e = configure<256>();
   return e;
 }
 
 int attention_tc_rows(int D) { return D == 256 ? 128 : 256; }
 
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st) {
-  const bool f8 = (c.pre.len && c.pre_f8) || (!c.plan.decode && c.own.len && c.own_f8);
-  if (f8)
-    return c.D == 64 ? launch_tc<64, true>(c, st) : c.D == 128 ? launch_tc<128, true>(c, st) : launch_tc<256, true>(c, st);
-  return c.D == 64 ? launch_tc<64, false>(c, st) : c.D == 128 ? launch_tc<128, false>(c, st) : launch_tc<256, false>(c, st);
+  return c.D == 64 ? launch_tc<64>(c, st) : c.D == 128 ? launch_tc<128>(c, st) : launch_tc<256>(c, st);
 }
 
 }  // namespace rtv

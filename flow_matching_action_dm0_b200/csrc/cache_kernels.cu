@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Ca
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (r0 + k * RPB + threadIdx.x / LPR >= rows) continue;
+      if (r0 + k * RPB + threadIdx.x / LPR >= rows || (c.skip && (long long)c.first + t[k] >= n)) continue;
       const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       float x[16];
 #pragma unroll
@@ -428,10 +428,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 }
 
 template <int D, int BM>
-cudaError_t launch_f32(const AttnCall& c, cudaStream_t st) {
-  const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + (long long)c.B * c.plan.tiles_e * c.plan.ne), c.Hkv);
-  attn_f32_kernel<D, BM><<<grid, 256, attn_f32_smem(BM, D), st>>>(c);
+cudaError_t launch_f32_units(AttnCall& c, unsigned first, long long units, cudaStream_t st) {
+  if (units == 0) return cudaSuccess;
+  c.unit0 = first;
+  attn_f32_kernel<D, BM><<<dim3((unsigned)units, c.Hkv), 256, attn_f32_smem(BM, D), st>>>(c);
   return cudaGetLastError();
+}
+// Stacked and element units may have different rows: a launch each.
+template <int D>
+cudaError_t launch_f32(AttnCall& c, cudaStream_t st) {
+  const AttnPlan& p = c.plan;
+  const long long ns = (long long)p.tiles_s * p.ns, ne = (long long)c.B * p.tiles_e * p.ne;
+  cudaError_t e = p.bm_s == 16 ? launch_f32_units<D, 16>(c, 0, ns, st) : launch_f32_units<D, 64>(c, 0, ns, st);
+  if (e == cudaSuccess)
+    e = p.bm_e == 16 ? launch_f32_units<D, 16>(c, (unsigned)ns, ne, st) : launch_f32_units<D, 64>(c, (unsigned)ns, ne, st);
+  c.unit0 = 0;
+  return e;
 }
 
 template <typename QT, int D>
@@ -452,7 +464,7 @@ cudaError_t launch_combine(const AttnCall& c, cudaStream_t st) {
 template <int D>
 cudaError_t launch_all(AttnCall& c, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (!c.bf16) e = c.plan.bm_e == 16 ? launch_f32<D, 16>(c, st) : launch_f32<D, 64>(c, st);
+  if (!c.bf16) e = launch_f32<D>(c, st);
   if (c.bf16 && (c.plan.ns || !c.plan.decode)) e = launch_attention_tc(c, st);
   if (e == cudaSuccess && c.plan.decode && c.plan.ne) {
     c.unit0 = (unsigned)c.plan.tiles_s * c.plan.ns;
@@ -501,48 +513,138 @@ cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
          : c.dim == 128 ? read_d<float, 128>(c, grid, st) : read_d<float, 256>(c, grid, st);
 }
 
+// How many key ranges a unit's tiles are split over, and about how long the
+// launch then takes (us).  `fixed` is a CTA's start and end, `tile` a key tile;
+// a second range brings the join: its launch, and every row's parts written
+// and read.  (Measured on B200: 64 units of 128 rows x 7 tiles of head_dim 256
+// take 24.6 us in two ranges and their join, 18 us in one.)
+struct Split {
+  int n;
+  float us;
+};
+static Split best_split(long long units, int tiles, int slots, float fixed, float tile, float join, float join_each) {
+  Split best{1, 1e30f};
+  for (int n = 1; n <= std::min(std::max(tiles, 1), 64); ++n) {
+    const long long waves = (units * n + slots - 1) / slots;
+    const float us = (float)waves * (fixed + (float)((tiles + n - 1) / n) * tile) + (n > 1 ? join : 0.f) + join_each * n;
+    if (us < best.us) best = {n, us};
+  }
+  return best;
+}
+
 AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   AttnPlan p{};
   p.rows_b = c.Tq * c.group;
   p.cluster = 1;
-  // The few-row kernel reads one type; a prefix and own keys meet in it only without stacking.
-  p.decode = c.bf16 && p.rows_b <= kDecodeRows && (c.B > 1 || !c.pre.len || !c.own.len || c.pre_f8 == c.own_f8);
-  const int most = c.bf16 ? attention_tc_rows(c.D) : 64;             // rows of a CTA
-  p.bm_e = p.decode ? kDecodeRows : c.bf16 ? most : p.rows_b <= 16 ? 16 : 64;
-  p.bm_s = c.bf16 ? most : p.bm_e;
-  p.kt_s = c.bf16 ? 128 : kKeys;
-  p.kt_e = p.decode ? 16 * decode_groups(c.D) : p.kt_s;
+  p.decode = c.bf16 && p.rows_b <= kDecodeRows;
   // Rows of several elements share a tile (and its pass over the prefix) when
   // one element's rows would leave half of it empty.
-  const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : p.bm_e / 2);
-  const int tb = (p.rows_b + p.bm_e - 1) / p.bm_e;
-  // key ranges of `units` x heads units so that `slots` CTAs run at once
-  auto split = [&](long long units, int keys, int kt, int slots) {
-    const int tiles = (keys + kt - 1) / kt;
-    return (int)std::max(1LL, std::min<long long>({slots / (units * c.Hkv), tiles, 64}));
-  };
-  if (stack) {
-    p.tiles_s = (int)(((long long)c.B * p.rows_b + p.bm_s - 1) / p.bm_s);
-    p.ns = split(p.tiles_s, c.pre.len, p.kt_s, c.bf16 ? num_sms : 2 * num_sms);
-  }
+  const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : 16);
   p.prefix_in_elem = c.pre.len > 0 && !stack;
+  // E4M3: the few-row kernel reads one source of codes itself; the others are
+  // read back to bf16 first, once for all of the rows that go over them.
+  const bool codes = p.decode && !stack && (!c.pre.len || !c.own.len);
+  p.unpack_pre = c.bf16 && c.pre.len > 0 && c.pre_f8 && !codes;
+  p.unpack_own = c.bf16 && c.own.len > 0 && c.own_f8 && !codes;
+  const long long rows = (long long)c.B * p.rows_b;
+  const float join = 3.f, join_each = (float)(rows * c.Hkv * c.D) * 8.f / 4e6f;   // us: launch; a part of all rows at 4 TB/s
+  auto tiles_of = [](long long keys, int kt) { return (int)((keys + kt - 1) / kt); };
+  // Rows of a unit and its ranges, for `elems` elements of `rows_e` rows over `keys` keys.
+  auto shape = [&](long long elems, long long rows_e, long long keys, int kt, int* bm, int* tiles, int* n) {
+    float best = 1e30f;
+    const int choices[2] = {c.bf16 ? 128 : 16, c.bf16 ? attention_tc_rows(c.D) : 64};
+    for (const int rows_u : choices) {
+      const long long tu = (rows_e + rows_u - 1) / rows_u;
+      float fixed, tile;
+      int slots;
+      if (c.bf16) {
+        // two row tiles share a CTA's loads
+        fixed = 5.f;
+        tile = c.D == 256 ? 1.15f : c.D == 128 ? (rows_u == 256 ? 1.95f : 1.1f) : (rows_u == 256 ? 1.5f : 0.9f);
+        slots = num_sms;
+      } else {
+        fixed = 2.5f;
+        tile = (rows_u == 64 ? 2.6f : 1.2f) * (float)c.D / 64.f;
+        slots = num_sms * std::max(1, 227 * 1024 / (attn_f32_smem(rows_u, c.D) + 1024));
+      }
+      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), slots, fixed, tile, join, join_each);
+      if (s.us < best) {
+        best = s.us;
+        *bm = rows_u;
+        *tiles = (int)tu;
+        *n = s.n;
+      }
+    }
+  };
+  p.kt_s = c.bf16 ? 128 : kKeys;
+  p.kt_e = p.decode ? 16 * decode_groups(c.D) : p.kt_s;
+  p.bm_s = c.bf16 ? 128 : 64;
+  if (stack) shape(1, rows, c.pre.len, p.kt_s, &p.bm_s, &p.tiles_s, &p.ns);
   if (!stack || c.own.len > 0) {
-    const int keys = c.own.len + (p.prefix_in_elem ? c.pre.len : 0);
-    p.tiles_e = tb;
-    p.ne = split((long long)c.B * tb, keys, p.kt_e, p.decode ? attention_decode_ctas(c.D) * num_sms : c.bf16 ? num_sms : 2 * num_sms);
-    // Up to eight ranges join in a cluster, without a second launch.
-    if (p.decode && !stack && p.ne > 1) {
-      if (p.ne <= 16) p.ne = std::min(p.ne, 8);
-      if (p.ne <= 8) p.cluster = p.ne;
+    const long long keys = (long long)c.own.len + (p.prefix_in_elem ? c.pre.len : 0);
+    if (p.decode) {
+      p.bm_e = kDecodeRows;
+      p.tiles_e = 1;
+      const long long units = (long long)c.B * c.Hkv, slots = (long long)attention_decode_ctas(c.D) * num_sms;
+      p.ne = (int)std::max(1LL, std::min<long long>({slots / units, tiles_of(keys, p.kt_e), 64}));
+      // Up to eight ranges join in a cluster, without a second launch.
+      if (!stack && p.ne > 1) {
+        if (p.ne <= 16) p.ne = std::min(p.ne, 8);
+        if (p.ne <= 8) p.cluster = p.ne;
+      }
+    } else {
+      shape(c.B, p.rows_b, keys, p.kt_e, &p.bm_e, &p.tiles_e, &p.ne);
     }
   }
   p.n_slots = p.cluster > 1 ? 1 : p.ns + p.ne;
   return p;
 }
 
-size_t attention_workspace(const AttnCall& c) {
+namespace {
+size_t round_256(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t part_bytes(const AttnCall& c) {
   if (c.plan.n_slots <= 1) return 0;
-  return (size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * (size_t)(c.D + 2) * 4;
+  return round_256((size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * (size_t)(c.D + 2) * 4);
+}
+// K (and as much V) of a source in bf16.
+size_t unpacked_bytes(const AttnCall& c, const KvSource& s, int batch) {
+  return round_256((size_t)batch * c.Hkv * s.len * c.D * 2);
+}
+// Reads a source back to bf16 at `to`, dense [batch][head][token][D], and points the call at it.
+cudaError_t unpack(const AttnCall& c, KvSource& s, int batch, char* to, cudaStream_t st) {
+  const size_t bytes = unpacked_bytes(c, s, batch);
+  CacheCall r{};
+  r.rows.base = to;
+  r.rows.outer_bytes = (long long)bytes;
+  r.rows.sh = (long long)s.len * c.D;
+  r.rows.sb = r.rows.sh * c.Hkv;
+  r.rows.st = c.D;
+  r.cache.codes = (uint8_t*)s.k;
+  r.cache.codes_outer = (const char*)s.v - (const char*)s.k;
+  r.cache.scales = (float*)s.ks;
+  r.cache.scales_outer = (const char*)s.vs - (const char*)s.ks;
+  r.cache.sb = s.sb, r.cache.st = s.st, r.cache.sh = s.sh;
+  r.cache.fb = s.fb, r.cache.ft = s.ft, r.cache.fh = s.fh;
+  r.outer = 2;
+  r.batch = batch;
+  r.tokens = r.capacity = s.len;
+  r.heads = c.Hkv;
+  r.dim = c.D;
+  r.bf16 = 1;
+  r.lens = s.lens;
+  r.skip = 1;
+  r.status = c.status;
+  s.k = to;
+  s.v = to + bytes;
+  s.ks = s.vs = nullptr;
+  s.sb = r.rows.sb, s.st = r.rows.st, s.sh = r.rows.sh;
+  return launch_kv_read(r, st);
+}
+}  // namespace
+
+size_t attention_workspace(const AttnCall& c) {
+  return part_bytes(c) + (c.plan.unpack_pre ? 2 * unpacked_bytes(c, c.pre, 1) : 0) +
+         (c.plan.unpack_own ? 2 * unpacked_bytes(c, c.own, c.B) : 0);
 }
 
 cudaError_t configure_attention() {
@@ -560,8 +662,22 @@ cudaError_t configure_attention() {
 }
 
 cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st) {
-  c.part_o = (float*)workspace;
+  char* at = (char*)workspace;
+  c.part_o = (float*)at;
   c.part_ml = c.part_o + (size_t)c.Hkv * c.plan.n_slots * ((size_t)c.B * c.plan.rows_b) * c.D;
+  at += part_bytes(c);
+  cudaError_t e = cudaSuccess;
+  if (c.plan.unpack_pre) {
+    const size_t bytes = 2 * unpacked_bytes(c, c.pre, 1);
+    e = unpack(c, c.pre, 1, at, st);
+    at += bytes;
+    c.pre_f8 = 0;
+  }
+  if (e == cudaSuccess && c.plan.unpack_own) {
+    e = unpack(c, c.own, c.B, at, st);
+    c.own_f8 = 0;
+  }
+  if (e != cudaSuccess) return e;
   return c.D == 64 ? launch_all<64>(c, st) : c.D == 128 ? launch_all<128>(c, st) : launch_all<256>(c, st);
 }
 

@@ -40,6 +40,7 @@ struct AttnPlan {
   int prefix_in_elem;          // element units read the prefix too
   int decode;                  // element units are the few-row kernel's
   int cluster;                 // its CTAs that join by distributed shared memory (1: none)
+  int unpack_pre, unpack_own;  // E4M3 sources that are read back to bf16 in the workspace first
   int n_slots;                 // partial results of a row
 };
 
@@ -103,6 +104,7 @@ struct CacheCall {
   int first;
   const int* start;            // write: [batch] or nullptr
   const int* lens;             // write: count; read: valid tokens ([batch] or nullptr)
+  int skip;                    // read: tokens behind the valid ones are left as they are, not zeroed
   unsigned* status;
 };
 cudaError_t launch_kv_write(const CacheCall& c, cudaStream_t st);
