@@ -68,11 +68,12 @@ struct Cfg {
   static_assert(kSmem <= 232448 - 64, "shared memory of a CTA");
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int t, int h, int b, uint64_t* bar) {
+// A box of [64 dims, tokens from t, 64-dim chunks from ch] of head h, element b.
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int t, int ch, int h, int b, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
           ptx::smem_u32(dst)),
-      "l"(map), "r"(x), "r"(t), "r"(h), "r"(b), "r"(ptx::smem_u32(bar))
+      "l"(map), "r"(0), "r"(t), "r"(ch), "r"(h), "r"(b), "r"(ptx::smem_u32(bar))
       : "memory");
 }
 
@@ -285,28 +286,28 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     return false;
   };
-  // One load of the order: the boxes of a stage, K chunk or V keys.
-  auto load = [&](int o, int cc, uint8_t* dst, uint64_t* bar) {
-    const TileAt t = tile_at(u, u.t0 + (o >> 1));
-    const CUtensorMap* map = t.pre ? ((o & 1) ? &maps.pre_v : &maps.pre_k) : ((o & 1) ? &maps.own_v : &maps.own_k);
-    const int h = u.kvh * (t.pre ? maps.pre_h : maps.own_h), b = t.pre ? 0 : u.b * maps.own_b;
-    ptx::mbar_expect_tx(bar, (uint32_t)kStage);
-    if (!(o & 1)) {
-      tma_load_4d(dst, map, 64 * cc, t.k0, h, b, bar);
-    } else {
-#pragma unroll
-      for (int dc = 0; dc < NC; ++dc) tma_load_4d(dst + dc * VK * 128, map, 64 * dc, t.k0 + cc * VK, h, b, bar);
-    }
-  };
   if (warp == 0) {
     // ---- loads ---------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
+      const int pre_h = u.kvh * maps.pre_h, own_h = u.kvh * maps.own_h, own_b = u.b * maps.own_b;
       bool ok = true;
-      for (int i = 0; i < 2 * n * NC && ok; ++i) {
-        const int s = i % NST;
-        ok = wait(&empty[s], i / NST + 1);
-        if (ok) load(order.at(i / NC), i % NC, ring + s * kStage, &ready[s]);
+      int s = 0, ph = 1;
+      for (int i = 0; i < 2 * n && ok; ++i) {
+        const int o = order.at(i);
+        const TileAt t = tile_at(u, u.t0 + (o >> 1));
+        const CUtensorMap* map = (o & 1) ? (t.pre ? &maps.pre_v : &maps.own_v) : (t.pre ? &maps.pre_k : &maps.own_k);
+        const int h = t.pre ? pre_h : own_h, b = t.pre ? 0 : own_b;
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+          ok = ok && wait(&empty[s], ph);
+          if (!ok) break;
+          ptx::mbar_expect_tx(&ready[s], (uint32_t)kStage);
+          // a K stage is a chunk of 64 dims of 128 keys, a V stage all dims of VK keys
+          if (o & 1) tma_load(ring + s * kStage, map, t.k0 + cc * VK, 0, h, b, &ready[s]);
+          else tma_load(ring + s * kStage, map, t.k0, cc, h, b, &ready[s]);
+          if (++s == NST) s = 0, ph ^= 1;
+        }
       }
     }
     __syncwarp();
@@ -333,60 +334,75 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (++s == NST) s = 0, ++ph;
         }
       };
+      // Where the ring holds the next K beside the K in use, loads are awaited
+      // ahead, so that a product and the next scores are issued in one run;
+      // otherwise each stage is awaited as its turn comes.
+      constexpr bool kAhead = 3 * NC <= NST;
+      auto stage_landed = [&](int s, int ph) {
+        if (kAhead) return;
+        ok = ok && wait(&ready[s], ph);
+        ptx::tc_fence_after();
+      };
       auto scores = [&](int q) {                  // S(q), over P(q - 2), whose MMA comes before it in this thread's order
-        const int buf = q & 1, rt = two ? buf : 0;
-        int s = (order.of_k(two ? q >> 1 : q) * NC) % NST;
-        if (leader && ok) {
+        const int buf = q & 1, rt = two ? buf : 0, pos = order.of_k(two ? q >> 1 : q) * NC;
+        int s = pos % NST, ph = pos / NST;
 #pragma unroll
-          for (int cc = 0; cc < NC; ++cc) {
+        for (int cc = 0; cc < NC; ++cc) {
+          stage_landed(s, ph);
+          if (leader && ok) {
             const uint32_t qa = q_lo + rt * (C::QB >> 4) + cc * (16384 >> 4), ka = k_lo + s * (kStage >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               ptx::umma_bf16(tmem + buf * kTile, desc64(qa + 2 * kk, s_hi), desc64(ka + 2 * kk, s_hi), id_s, (cc | kk) != 0);
             if (!two || rt == 1) ptx::umma_commit(&empty[s]);   // the key tile's last use
-            if (++s == NST) s = 0;
           }
+          if (++s == NST) s = 0, ++ph;
+        }
+        if (leader && ok) {
           ptx::umma_commit(&s_full[buf]);
         }
       };
       ok = wait(&q_ready[0], 0);
       if (!two) ok = wait(&q_ready[1], 0) && ok;
-      landed(order.of_k(0));
+      if (kAhead) landed(order.of_k(0));
       ptx::tc_fence_after();
       scores(0);
       if (steps > 1) {
         if (two) ok = wait(&q_ready[1], 0) && ok;
-        else landed(order.of_k(1));
+        else if (kAhead) landed(order.of_k(1));
         ptx::tc_fence_after();
         scores(1);
       }
       for (int q = 0; q < steps && ok; ++q) {
         const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
-        if (rt == 0) {
-          landed(order.of_v(j));
-          if (((j < own0 ? pre_mask : own_mask) || j == pre_end || j == own_end) && leader && ok) ptx::mbar_arrive(&v_landed[buf]);
-        }
         const bool next = q + 2 < steps;
-        if (next && rt == 0) landed(order.of_k(two ? j + 1 : q + 2));
+        if (rt == 0) {
+          const bool hidden = (j < own0 ? pre_mask : own_mask) || j == pre_end || j == own_end;
+          if (kAhead || hidden) landed(order.of_v(j));
+          if (hidden && leader && ok) ptx::mbar_arrive(&v_landed[buf]);
+          if (kAhead && next) landed(order.of_k(two ? j + 1 : q + 2));
+        }
         ok = ok && wait(&p_ready[buf], q >> 1);
         ptx::tc_fence_after();
-        int s = (order.of_v(j) * NC) % NST;
-        if (leader && ok) {
+        const int pos = order.of_v(j) * NC;
+        int s = pos % NST, ph = pos / NST;
 #pragma unroll
-          for (int cc = 0; cc < NC; ++cc) {
+        for (int cc = 0; cc < NC; ++cc) {
+          stage_landed(s, ph);
+          if (leader && ok) {
             const uint32_t va = v_lo + s * (kStage >> 4);
 #pragma unroll
             for (int kk = 0; kk < VK / 16; ++kk)
               umma_bf16_ts(o_tmem + rt * kTile, tmem + buf * kTile + (cc * VK + kk * 16) / 2, desc64(va + kk * (2048 >> 4), v_hi),
                            id_o, (j | cc | kk) != 0);
             if (!two || rt == 1) ptx::umma_commit(&empty[s]);
-            if (++s == NST) s = 0;
           }
+          if (++s == NST) s = 0, ++ph;
+        }
+        if (leader && ok) {
           if (!two) ptx::umma_commit(pv_done);
         }
-        if (next) {
-          scores(q + 2);
-        }
+        if (next) scores(q + 2);
       }
       // every MMA completes before the tensor memory is read for the last time and freed
       if (leader) {
@@ -657,15 +673,16 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of one tensor [batch][token][head][D] with boxes of 64 dims x `keys` tokens.
-bool encode(CUtensorMap* m, const void* base, int D, int keys, int len, int heads, long long st, long long sh, int batch,
-            long long sb) {
+// Map of one tensor [batch][token][head][D] as [batch][head][64-dim chunk][token][64], with boxes of `keys` tokens of
+// `chunks` chunks: a box lies in shared memory chunk by chunk, rows of 128 bytes.
+bool encode(CUtensorMap* m, const void* base, int D, int chunks, int keys, int len, int heads, long long st, long long sh,
+            int batch, long long sb) {
   const long long dense = 2LL * D;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)len, (cuuint64_t)heads, (cuuint64_t)batch};
-  const cuuint64_t strides[3] = {(cuuint64_t)(len > 1 ? 2 * st : dense), (cuuint64_t)(heads > 1 ? 2 * sh : dense),
+  const cuuint64_t dims[5] = {64, (cuuint64_t)len, (cuuint64_t)(D / 64), (cuuint64_t)heads, (cuuint64_t)batch};
+  const cuuint64_t strides[4] = {(cuuint64_t)(len > 1 ? 2 * st : dense), 128, (cuuint64_t)(heads > 1 ? 2 * sh : dense),
                                  (cuuint64_t)(batch > 1 ? 2 * sb : dense)};
-  const cuuint32_t box[4] = {64, (cuuint32_t)keys, 1, 1}, one[4] = {1, 1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+  const cuuint32_t box[5] = {64, (cuuint32_t)keys, (cuuint32_t)chunks, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, one,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -680,8 +697,8 @@ cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
     *hm = c.Hkv > 1 && s.sh == 0 ? 0 : 1;
     *bm = batch > 1 && s.sb == 0 ? 0 : 1;
     const int heads = *hm ? c.Hkv : 1, nb = *bm ? batch : 1;
-    ok = ok && encode(k, s.k, D, kTile, s.len, heads, s.st, s.sh, nb, s.sb) &&
-         encode(v, s.v, D, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
+    ok = ok && encode(k, s.k, D, 1, kTile, s.len, heads, s.st, s.sh, nb, s.sb) &&
+         encode(v, s.v, D, C::NC, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
   };
   int pre_b = 0;
   source(c.pre, 1, &m.pre_k, &m.pre_v, &m.pre_h, &pre_b);
