@@ -170,18 +170,18 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Ca
 // fp32 attention: BM rows against tiles of 64 keys, 256 threads as 16 x 16;
 // thread (ty, tx) holds rows ty + 16 i, keys tx + 16 j of the scores and
 // columns 4 tx + 64 c of the output.  One pass over the keys with the running
-// maximum (base 2) and sum of each row.  Hidden keys score -inf and their
-// values are read as zeros, whatever they hold.
+// maximum (base 2) and sum of each row.  The next keys are copied while the
+// values are used and the next values while the keys are.  Hidden keys score
+// -inf and are copied as zeros, whatever they hold.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
 __host__ __device__ constexpr int attn_f32_smem(int bm, int d) {
-  return 4 * (bm * (d + 4) + kKeys * (d + 4) + kKeys * d + bm * (kKeys + 4) + kKeys);
+  return 4 * (bm * (d + 4) + kKeys * (d + 4) + kKeys * d + bm * (kKeys + 4) + 2 * kKeys);
 }
 
-// Four elements of a key or value row: fp32, or E4M3 codes times the row's scale.
-__device__ __forceinline__ float4 load_kv4(const void* base, const float* scales, bool f8, long long off, long long foff) {
-  if (!f8) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
+// Four E4M3 codes of a key or value row times the row's scale.
+__device__ __forceinline__ float4 load_codes4(const void* base, const float* scales, long long off, long long foff) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) + off);
   const float s = scales[foff];
   const float2 a = e4m3x2_to_f32x2(w & 0xFFFFu), b = e4m3x2_to_f32x2(w >> 16);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
   float* Ks = Qs + BM * LD;
   float* Vs = Ks + kKeys * LD;
   float* Ps = Vs + kKeys * D;
-  float* Ok = Ps + BM * LP;       // 1: the tile's key is seen
+  float* Ok = Ps + BM * LP;       // [2][kKeys] 1: the tile's key is seen
   const AttnUnit u = attn_unit(c);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ptx::pdl_launch_dependents();   // (combine_kernel waits for this grid's end before it reads)
@@ -224,36 +224,55 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
     for (int k = 0; k < D / 64; ++k) acc[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
-  for (int tile = u.t0; tile < u.t1; ++tile) {
+  auto look = [&](int tile) {     // which keys of a tile are seen
+    if (tile >= u.t1 || tid >= kKeys) return;
     const bool pre = tile < u.n0;
-    const KvSource& s = pre ? c.pre : c.own;
-    const bool f8 = pre ? c.pre_f8 : c.own_f8;
-    const int bb = pre ? 0 : u.b;
-    const int k0 = (pre ? tile : tile - u.n0) * kKeys;
-    const int nk = min(kKeys, (pre ? u.len0 : u.len1) - k0);
-    __syncthreads();
-    if (tid < kKeys) Ok[tid] = tid < nk && (!s.mask || s.mask[bb * s.mask_sb + k0 + tid]) ? 1.f : 0.f;
-    __syncthreads();
+    const int k = (pre ? tile : tile - u.n0) * kKeys + tid;
+    const uint8_t* mask = pre ? c.pre.mask : c.own.mask ? c.own.mask + u.b * c.own.mask_sb : nullptr;
+    Ok[(tile & 1) * kKeys + tid] = k < (pre ? u.len0 : u.len1) && (!mask || mask[k]) ? 1.f : 0.f;
+  };
+  auto copy = [&](int tile, bool val) {   // its keys or values (after look and a barrier); one commit group
+    if (tile < u.t1) {
+      const bool pre = tile < u.n0, f8 = pre ? c.pre_f8 : c.own_f8;
+      const int k0 = (pre ? tile : tile - u.n0) * kKeys;
+      const long long st = pre ? c.pre.st : c.own.st, ft = pre ? c.pre.ft : c.own.ft;
+      const long long base = (pre ? 0 : u.b * c.own.sb) + k0 * st + u.kvh * (pre ? c.pre.sh : c.own.sh);
+      const long long fbase = (pre ? 0 : u.b * c.own.fb) + k0 * ft + u.kvh * (pre ? c.pre.fh : c.own.fh);
+      const void* src = pre ? (val ? c.pre.v : c.pre.k) : (val ? c.own.v : c.own.k);
+      const float* scales = pre ? (val ? c.pre.vs : c.pre.ks) : (val ? c.own.vs : c.own.ks);
+      float* dst = val ? Vs : Ks;
+      const int ld = val ? D : LD;
 #pragma unroll 4
-    for (int i = tid; i < kKeys * C4; i += 256) {
-      const int r = i / C4, d = (i - r * C4) * 4;
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (Ok[r] != 0.f) {
-        const long long off = bb * s.sb + (long long)(k0 + r) * s.st + u.kvh * s.sh + d;
-        const long long foff = bb * s.fb + (long long)(k0 + r) * s.ft + u.kvh * s.fh;
-        kv = load_kv4(s.k, s.ks, f8, off, foff);
-        vv = load_kv4(s.v, s.vs, f8, off, foff);
+      for (int i = tid; i < kKeys * C4; i += 256) {
+        const int r = i / C4, d = (i - r * C4) * 4;
+        const bool on = Ok[(tile & 1) * kKeys + r] != 0.f;
+        if (f8) {
+          *reinterpret_cast<float4*>(dst + r * ld + d) =
+              on ? load_codes4(src, scales, base + r * st + d, fbase + r * ft) : make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+          const float* from = reinterpret_cast<const float*>(src) + (on ? base + r * st + d : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst + r * ld + d)), "l"(from), "r"(on ? 16 : 0)
+                       : "memory");
+        }
       }
-      *reinterpret_cast<float4*>(Ks + r * LD + d) = kv;
-      *reinterpret_cast<float4*>(Vs + r * D + d) = vv;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  look(u.t0);
+  __syncthreads();
+  copy(u.t0, false);
+  copy(u.t0, true);
+  for (int tile = u.t0; tile < u.t1; ++tile) {
+    const float* ok = Ok + (tile & 1) * kKeys;
+    look(tile + 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys
     __syncthreads();
     float sc[TM][4];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll (TM == 1 ? 8 : 4)
     for (int d = 0; d < D; d += 4) {
       float4 qv[TM], kv[4];
 #pragma unroll
@@ -272,7 +291,7 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sc[i][j] = Ok[tx + 16 * j] != 0.f ? sc[i][j] * c.scale_log2 : -INFINITY;
+        sc[i][j] = ok[tx + 16 * j] != 0.f ? sc[i][j] * c.scale_log2 : -INFINITY;
         top = fmaxf(top, sc[i][j]);
       }
 #pragma unroll
@@ -297,8 +316,11 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
         acc[i][k].w *= corr;
       }
     }
-    __syncwarp();   // a row's weights are written and read by the same half-warp
-#pragma unroll 2
+    __syncthreads();              // (a row's weights are written and read by the same half-warp) the keys are done with
+    copy(tile + 1, false);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values
+    __syncthreads();
+#pragma unroll (TM == 1 ? 4 : 2)
     for (int k4 = 0; k4 < kKeys; k4 += 4) {
       float4 p[TM];
 #pragma unroll
@@ -319,6 +341,8 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
         }
       }
     }
+    __syncthreads();              // the values are done with
+    copy(tile + 1, true);
   }
 
 #pragma unroll
@@ -514,19 +538,21 @@ cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
 }
 
 // How many key ranges a unit's tiles are split over, and about how long the
-// launch then takes (us).  `fixed` is a CTA's start and end, `tile` a key tile;
-// a second range brings the join: its launch, and every row's parts written
+// launch then takes (us).  `fixed` is a CTA's start and end, `tile` a key tile
+// at an SM's full rate and `alone` with one CTA on it; a second range brings the join: its launch, and every row's parts written
 // and read.  (Measured on B200: 64 units of 128 rows x 7 tiles of head_dim 256
 // take 24.6 us in two ranges and their join, 18 us in one.)
 struct Split {
   int n;
   float us;
 };
-static Split best_split(long long units, int tiles, int slots, float fixed, float tile, float join, float join_each) {
+static Split best_split(long long units, int tiles, int sms, int per_sm, float fixed, float tile, float alone, float join,
+                        float join_each) {
   Split best{1, 1e30f};
   for (int n = 1; n <= std::min(std::max(tiles, 1), 64); ++n) {
-    const long long waves = (units * n + slots - 1) / slots;
-    const float us = (float)waves * (fixed + (float)((tiles + n - 1) / n) * tile) + (n > 1 ? join : 0.f) + join_each * n;
+    const long long ctas = units * n, waves = (ctas + (long long)sms * per_sm - 1) / ((long long)sms * per_sm);
+    const float shared = (float)std::min<long long>(per_sm, (ctas + sms - 1) / sms) * tile;   // CTAs of an SM share its rate
+    const float us = (float)waves * (fixed + (float)((tiles + n - 1) / n) * std::max(alone, shared)) + (n > 1 ? join : 0.f) + join_each * n;
     if (us < best.us) best = {n, us};
   }
   return best;
@@ -555,19 +581,19 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
     const int choices[2] = {c.bf16 ? 128 : 16, c.bf16 ? attention_tc_rows(c.D) : 64};
     for (const int rows_u : choices) {
       const long long tu = (rows_e + rows_u - 1) / rows_u;
-      float fixed, tile;
-      int slots;
+      float fixed, tile, alone;
+      int per_sm = 1;
       if (c.bf16) {
         // two row tiles share a CTA's loads
-        fixed = 5.f;
-        tile = c.D == 256 ? 1.15f : c.D == 128 ? (rows_u == 256 ? 1.95f : 1.1f) : (rows_u == 256 ? 1.5f : 0.9f);
-        slots = num_sms;
+        fixed = 6.f;
+        tile = alone = c.D == 256 ? 1.5f : c.D == 128 ? (rows_u == 256 ? 1.95f : 1.1f) : (rows_u == 256 ? 1.5f : 0.9f);
       } else {
-        fixed = 2.5f;
-        tile = (rows_u == 64 ? 2.6f : 1.2f) * (float)c.D / 64.f;
-        slots = num_sms * std::max(1, 227 * 1024 / (attn_f32_smem(rows_u, c.D) + 1024));
+        fixed = 4.f;
+        tile = (rows_u == 64 ? 2.6f : 1.f) * (float)c.D / 64.f;
+        alone = (rows_u == 64 ? 4.5f : 3.f) * (float)c.D / 64.f;
+        per_sm = std::max(1, 227 * 1024 / (attn_f32_smem(rows_u, c.D) + 1024));
       }
-      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), slots, fixed, tile, join, join_each);
+      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), num_sms, per_sm, fixed, tile, alone, join, join_each);
       if (s.us < best) {
         best = s.us;
         *bm = rows_u;
