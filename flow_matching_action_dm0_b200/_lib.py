@@ -33,7 +33,7 @@ EXPORTS = ("rtv_create", "rtv_load_expert", "rtv_set_prefix_kv", "rtv_denoise", 
            "rtv_prefill_device_status", "rtv_prefill_last_error", "rtv_prefill_kernel_count", "rtv_prefill_destroy",
            "rtv_ops_create", "rtv_kv_write", "rtv_kv_read", "rtv_cross_attention", "rtv_cross_attention_workspace",
            "rtv_shared_attention", "rtv_shared_attention_workspace", "rtv_ops_device_status", "rtv_ops_last_error",
-           "rtv_ops_destroy")
+           "rtv_ops_destroy", "rtv_denoise_shared", "rtv_get_prefix_kv_quantized", "rtv_set_prefix_kv_quantized")
 
 
 class rtv_expert_config(C.Structure):
@@ -115,6 +115,9 @@ def load_library(path: str = LIB_PATH):
     lib.rtv_set_prefix_kv_static.argtypes = [P, P, I, I, P]
     lib.rtv_denoise.argtypes = [P, P, P, I, P, P]
     lib.rtv_verify.argtypes = [P, P, P, P, P, I, F, I, P, P, P, P]
+    lib.rtv_denoise_shared.argtypes = [P, P, P, I, I, P, P]
+    lib.rtv_get_prefix_kv_quantized.argtypes = [P, P, P, I, I, P]
+    lib.rtv_set_prefix_kv_quantized.argtypes = [P, P, P, I, I, P]
     lib.rtv_device_status.argtypes = [P, U]
     lib.rtv_last_error.argtypes = [P]
     lib.rtv_last_error.restype = C.c_char_p
@@ -163,7 +166,8 @@ def load_library(path: str = LIB_PATH):
     lib.rtv_ops_destroy.restype = None
     for n in ("rtv_ops_create", "rtv_kv_write", "rtv_kv_read", "rtv_cross_attention",
               "rtv_cross_attention_workspace", "rtv_shared_attention", "rtv_shared_attention_workspace",
-              "rtv_ops_device_status"):
+              "rtv_ops_device_status", "rtv_denoise_shared", "rtv_get_prefix_kv_quantized",
+              "rtv_set_prefix_kv_quantized"):
         getattr(lib, n).restype = I
     for n in ("rtv_create", "rtv_load_expert", "rtv_set_prefix_kv", "rtv_set_prefix_kv_static", "rtv_denoise",
               "rtv_verify", "rtv_device_status", "rtv_draft_create", "rtv_draft_load", "rtv_draft_forward",
@@ -209,6 +213,21 @@ def rtv_set_prefix_kv_static(h, kv_ptr: int, prefix_len: int, batch: int, stream
 def rtv_denoise(h, noise_ptr: int, state_ptr: int, n_steps: int, out_ptr: int, stream: int = 0):
     return _check(h, load_library().rtv_denoise(h, C.c_void_p(noise_ptr), C.c_void_p(state_ptr), n_steps,
                                                 C.c_void_p(out_ptr), C.c_void_p(stream)))
+
+
+def rtv_denoise_shared(h, noise_ptr: int, state_ptr: int, n_chunks: int, n_steps: int, out_ptr: int, stream: int = 0):
+    return _check(h, load_library().rtv_denoise_shared(h, C.c_void_p(noise_ptr), C.c_void_p(state_ptr), n_chunks,
+                                                       n_steps, C.c_void_p(out_ptr), C.c_void_p(stream)))
+
+
+def rtv_get_prefix_kv_quantized(h, codes_ptr: int, scales_ptr: int, prefix_len: int, batch: int, stream: int = 0):
+    return _check(h, load_library().rtv_get_prefix_kv_quantized(h, C.c_void_p(codes_ptr), C.c_void_p(scales_ptr),
+                                                                prefix_len, batch, C.c_void_p(stream)))
+
+
+def rtv_set_prefix_kv_quantized(h, codes_ptr: int, scales_ptr: int, prefix_len: int, batch: int, stream: int = 0):
+    return _check(h, load_library().rtv_set_prefix_kv_quantized(h, C.c_void_p(codes_ptr), C.c_void_p(scales_ptr),
+                                                                prefix_len, batch, C.c_void_p(stream)))
 
 
 def rtv_verify(h, draft_ptr, noise_ptr, state_ptr, taus_ptr, n_taus, delta, gripper_dim, acc_ptr, flags_ptr,

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     } else {
       const int t = r / c.group, h = u.kvh * c.group + r - t * c.group;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(c.out) + u.b * c.ob + t * c.ot + h * c.oh + d) =
+      *reinterpret_cast<uint32_t*>(out_bf16(c, u.b, t, h, d)) =
           ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
       if (d == 0 && c.lse)
         c.lse[((long long)u.b * c.Tq + t) * c.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     }
     const int t = r / c.group, h = u.kvh * c.group + r - t * c.group;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(c.out) + u.b * c.ob + t * c.ot + h * c.oh + d) =
+    *reinterpret_cast<uint32_t*>(out_bf16(c, u.b, t, h, d)) =
         ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
     if (d == 0 && c.lse)
       c.lse[((long long)u.b * c.Tq + t) * c.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;

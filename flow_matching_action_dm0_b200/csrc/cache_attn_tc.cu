@@ -633,8 +633,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (mine) {
         if (split) {
           if (l != 0.f) bulk_store(c.part_o + pr * D + c0, stage, cols * 4);   // (the join does not read an empty part)
+        } else if (c.out_tiled_rows == 0) {
+          bulk_store(out_bf16(c, b, t_row, h_row, c0), stage, cols * 2);
         } else {
-          bulk_store(reinterpret_cast<__nv_bfloat16*>(c.out) + b * c.ob + t_row * c.ot + h_row * c.oh + c0, stage, cols * 2);
+          for (int d = 0; d < cols; d += 8)
+            *reinterpret_cast<uint4*>(out_bf16(c, b, t_row, h_row, c0 + d)) = *reinterpret_cast<const uint4*>(stage + d * 2);
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");

@@ -433,18 +433,16 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   const unsigned b = (unsigned)row / (unsigned)c.plan.rows_b, rr = (unsigned)row - b * (unsigned)c.plan.rows_b;
   const unsigned t = rr / (unsigned)c.group, h = kvh * c.group + rr - t * (unsigned)c.group;
   const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-  QT* dst = reinterpret_cast<QT*>(c.out) + b * c.ob + t * c.ot + h * c.oh + lane * V;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    if (sizeof(QT) == 4) {
+    const int d = 32 * V * i + lane * V;
 #pragma unroll
-      for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<float2*>(reinterpret_cast<float*>(dst) + 32 * V * i + e) =
+    for (int e = 0; e < V; e += 2) {
+      if (sizeof(QT) == 4)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(c.out) + b * c.ob + t * c.ot + h * c.oh + d + e) =
             make_float2(acc[i][e] * inv, acc[i][e + 1] * inv);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + 32 * V * i + e) = ptx::pack_bf16x2(acc[i][e] * inv, acc[i][e + 1] * inv);
+      else
+        *reinterpret_cast<uint32_t*>(out_bf16(c, b, t, h, d + e)) = ptx::pack_bf16x2(acc[i][e] * inv, acc[i][e + 1] * inv);
     }
   }
   if (c.lse && lane == 0)
@@ -705,6 +703,18 @@ cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   return c.D == 64 ? launch_all<64>(c, st) : c.D == 128 ? launch_all<128>(c, st) : launch_all<256>(c, st);
+}
+
+cudaError_t run_attention(AttnCall& c, int num_sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  c.plan = plan_attention(c, num_sms);
+  // fewer ranges where the caller's workspace holds no more parts
+  while (attention_workspace(c) > workspace_bytes && (c.plan.ns > 1 || c.plan.ne > 1)) {
+    int& n = c.plan.ns > c.plan.ne ? c.plan.ns : c.plan.ne;
+    --n;
+    c.plan.n_slots = c.plan.ns + c.plan.ne;
+  }
+  if (attention_workspace(c) > workspace_bytes) return cudaErrorInvalidValue;
+  return launch_attention(c, workspace, st);
 }
 
 }  // namespace rtv

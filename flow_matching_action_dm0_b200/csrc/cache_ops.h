@@ -70,6 +70,8 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms);
 size_t attention_workspace(const AttnCall& c);
 // Enqueues a planned call; workspace as above.
 cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st);
+// Plans and enqueues a call whose workspace is given; splits no keys where it is too small.
+cudaError_t run_attention(AttnCall& c, int num_sms, void* workspace, size_t workspace_bytes, cudaStream_t st);
 // Sets the kernels' attributes on the current device (outside any capture).
 cudaError_t configure_attention();
 // The tensor-core kernel (bf16 queries).
@@ -170,6 +172,15 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
     u.t1 = u.t0 + (int)each + ((unsigned)split < rest ? 1 : 0);
   }
   return u;
+}
+
+// Where elements d.. of a query's output go (bf16; d and the run within 8 elements).
+__device__ __forceinline__ __nv_bfloat16* out_bf16(const AttnCall& c, unsigned b, unsigned t, unsigned h, int d) {
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(c.out);
+  if (c.out_tiled_rows == 0) return o + b * c.ob + t * c.ot + h * c.oh + d;
+  // the projections' tiled input: [column / 64][row][64], 16-byte chunks permuted by the row
+  const unsigned row = b * c.Tq + t, col = h * c.D + d;
+  return o + ((size_t)(col >> 6) * c.out_tiled_rows + row) * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
 }
 
 // Where a row's partial result goes.

@@ -43,9 +43,11 @@ struct FoldedQueries {
 // The expert's layers over G suffixes (residual stream ctx->h); mod set for
 // RTV_TIME_ADARMS; fold set: layer 0 reads its query rows' tiles and
 // residual from fold and launches no QKV projection (tensor-core attention only).
+// one_prefix: the groups' attention to the one prefix of batch element 0 is
+// the shared-prefix operator (bidirectional mask only).
 rtv_status fast_layers(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, const float* rope_cs,
                        const float* rope_sn, cudaStream_t st, const ModTables* mod = nullptr,
-                       const FoldedQueries* fold = nullptr);
+                       const FoldedQueries* fold = nullptr, bool one_prefix = false);
 // Bytes of the four FoldedQueries buffers for G suffix groups.
 void folded_sizes(const rtv_ctx* ctx, int G, size_t bytes[4]);
 // Bare block: fill f for G suffixes whose residual rows are rows[t % n_src_rows]
@@ -71,6 +73,7 @@ rtv_status fast_block_embed(rtv_ctx* ctx, const float* rows, int n_src_rows, int
 // every layer's keys (RoPE at positions 0..P-1) and values into the prefix
 // cache of the expert ex (batch element 0) and its tensor-core tiles; the
 // last layer computes keys and values only.  rope_cs / rope_sn: [P][D/2].
+// Past 960 tokens the attention is the cross-attention operator.
 rtv_status fast_prefill(rtv_ctx* pre, rtv_ctx* ex, const __nv_bfloat16* emb, int P, const float* rope_cs,
                         const float* rope_sn, cudaStream_t st);
 void fast_destroy(rtv_ctx* ctx);

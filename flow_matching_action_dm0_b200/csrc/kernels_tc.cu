@@ -46,6 +46,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "cache_ops.h"
 #include "fastpath.h"
 #include "kernels.h"
 #include "runtime.h"
@@ -1629,6 +1630,7 @@ struct FastPath {
   // attention partial rows [Gmax][Hq][16][64][D] (the tensor-core kernel
   // indexes the same storage as [Gmax][Hq/2][16][128][D]) and their (max, sum)
   __nv_bfloat16* att_po = nullptr;
+  size_t att_po_bytes = 0;
   float* att_pml = nullptr;
   // tensor-core attention (head pairs sharing a KV head): tiled operands
   bool tc_attn = false;
@@ -1922,7 +1924,8 @@ rtv_status fast_create(rtv_ctx* ctx) {
   if (configure_gemm<GM_QKV>() != cudaSuccess || configure_gemm<GM_O>() != cudaSuccess ||
       configure_gemm<GM_GU>() != cudaSuccess || configure_gemm<GM_DOWN>() != cudaSuccess ||
       configure_attn<128>() != cudaSuccess || configure_attn<256>() != cudaSuccess ||
-      configure_attn_tc<128>() != cudaSuccess || configure_attn_tc<256>() != cudaSuccess) {
+      configure_attn_tc<128>() != cudaSuccess || configure_attn_tc<256>() != cudaSuccess ||
+      configure_attention() != cudaSuccess) {
     cudaGetLastError();
     return RTV_ERR_CUDA;
   }
@@ -1966,7 +1969,7 @@ rtv_status fast_create(rtv_ctx* ctx) {
   bool ok = alloc((void**)&fp->qb, T * ctx->Q * 2) && alloc((void**)&fp->ob, Tp * ctx->Q * 2) &&
             alloc((void**)&fp->mb, Tp * (size_t)k.mlp_dim * 2) && alloc((void**)&fp->hb, Tp * (size_t)k.width * 2) &&
             alloc((void**)&fp->ssp, T * (size_t)(k.width / 128) * 4) &&
-            alloc((void**)&fp->att_po, (size_t)ctx->Gmax * k.n_q_heads * 16 * 64 * k.head_dim * 2) &&
+            alloc((void**)&fp->att_po, fp->att_po_bytes = (size_t)ctx->Gmax * k.n_q_heads * 16 * 64 * k.head_dim * 2) &&
             alloc((void**)&fp->att_pml, (size_t)ctx->Gmax * k.n_q_heads * 16 * 64 * 2 * 4) &&
             alloc((void**)&fp->ksb, (size_t)ctx->Gmax * ctx->KV * S * 2) &&
             alloc((void**)&fp->vsb, (size_t)ctx->Gmax * ctx->KV * S * 2);
@@ -2287,8 +2290,7 @@ rtv_status fast_prefill(rtv_ctx* pre, rtv_ctx* ex, const __nv_bfloat16* emb, int
   const int S = pre->S;                       // query rows per attention group (64)
   const int G = (P + S - 1) / S;              // query groups
   const int T = P, n_mma = G * S;             // real token rows; rows of the tiled layouts
-  if (!fp || !xp || !xp->tc_attn || !fp->tc_attn || G > pre->Gmax || S != 64 || (P + 63) / 64 + 1 > 16 ||
-      (P + 63) / 64 > xp->ntile_max) {
+  if (!fp || !xp || !xp->tc_attn || !fp->tc_attn || G > pre->Gmax || S != 64 || (P + 63) / 64 > xp->ntile_max) {
     pre->last_error = "prefill shape not supported by the tensor-core path";
     return RTV_ERR_UNSUPPORTED;
   }
@@ -2339,9 +2341,13 @@ rtv_status fast_prefill(rtv_ctx* pre, rtv_ctx* ex, const __nv_bfloat16* emb, int
   base.h = pre->h;
   base.hb = fp->hb;
   base.ssp = fp->ssp;
-  base.qt = fp->qt;
-  base.kts = fp->kts;
-  base.vts = fp->vts;
+  const bool tiled_att = (P + 63) / 64 + 1 <= 16;   // every key tile has a rank of the tiled attention
+  base.q = fp->qb;
+  if (tiled_att) {
+    base.qt = fp->qt;
+    base.kts = fp->kts;
+    base.vts = fp->vts;
+  }
   base.rope_cs = rope_cs;
   base.rope_sn = rope_sn;
   base.m = fp->mb;
@@ -2409,7 +2415,33 @@ rtv_status fast_prefill(rtv_ctx* pre, rtv_ctx* ex, const __nv_bfloat16* emb, int
     if (last) break;
     atc.pkt = xp->pkt + (size_t)l * ptile_layer;
     atc.pvt = xp->pvt + (size_t)l * ptile_layer;
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !tiled_att) {
+      // every token's queries to the layer's keys in the expert's cache, straight into O's tiled input
+      AttnCall c{};
+      c.q = fp->qb;
+      c.out = fp->ob;
+      c.out_tiled_rows = n_mma;
+      c.qh = D;
+      c.qt = Q;
+      c.qb = (long long)P * Q;
+      c.bf16 = 1;
+      c.B = 1;
+      c.Tq = P;
+      c.Hq = k.n_q_heads;
+      c.Hkv = k.n_kv_heads;
+      c.group = c.Hq / c.Hkv;
+      c.D = D;
+      c.scale_log2 = atc.scale_log2;
+      c.own.k = kl;
+      c.own.v = kl + kv_layer;
+      c.own.st = D;
+      c.own.sh = (long long)kx.max_prefix_len * D;
+      c.own.sb = c.own.sh * k.n_kv_heads;
+      c.own.len = P;
+      c.status = pre->status;
+      c.timeout_ns = k.barrier_timeout_ns;
+      e = run_attention(c, fp->num_sms, fp->att_po, fp->att_po_bytes, st);
+    } else if (e == cudaSuccess)
       e = D == 256 ? launch_attn_tc<256>(atc, ntp + 1, G, fp->num_sms, st)
                    : launch_attn_tc<128>(atc, ntp + 1, G, fp->num_sms, st);
 
@@ -2469,7 +2501,7 @@ namespace {
 // qkv0_only, only layer 0's QKV projection is launched.
 rtv_status layers_impl(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, const float* rope_cs,
                        const float* rope_sn, cudaStream_t st, const ModTables* mod, const FoldedQueries* fold,
-                       bool qkv0_only) {
+                       bool qkv0_only, bool one_prefix = false) {
   FastPath* fp = ctx->fast;
   const rtv_expert_config& k = ctx->cfg;
   const int S = ctx->S, T = G * S, w = k.width, F = k.mlp_dim, D = k.head_dim, Q = ctx->Q, KV = ctx->KV;
@@ -2551,7 +2583,7 @@ rtv_status layers_impl(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, cons
   // tensor-core attention when the pair layout applies and every key tile has
   // a rank (RTV_ATTN=mma selects the warp-MMA kernel instead)
   const int ntp = (P + 63) / 64;
-  const bool tc_att = fast_tc_attention(ctx, P);
+  const bool tc_att = fast_tc_attention(ctx, P) && !one_prefix;
   AttnTcArgs atc{};
   if (tc_att) {
     base.qt = fp->qt;
@@ -2638,6 +2670,37 @@ rtv_status layers_impl(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, cons
       if (e == cudaSuccess)
         e = D == 256 ? launch_attn_tc<256>(atl, ntp + 1, G, fp->num_sms, st)
                      : launch_attn_tc<128>(atl, ntp + 1, G, fp->num_sms, st);
+    } else if (one_prefix) {
+      // row-major q and suffix keys and values, straight into O's tiled input
+      AttnCall c{};
+      c.q = fp->qb;
+      c.out = fp->ob;
+      c.out_tiled_rows = n_mma;
+      c.qh = D;
+      c.qt = (long long)k.n_q_heads * D;
+      c.qb = S * c.qt;
+      c.bf16 = 1;
+      c.B = G;
+      c.Tq = S;
+      c.Hq = k.n_q_heads;
+      c.Hkv = k.n_kv_heads;
+      c.group = c.Hq / c.Hkv;
+      c.D = D;
+      c.scale_log2 = at.scale_log2;
+      c.pre.k = (const __nv_bfloat16*)ctx->prefix_kv + (size_t)(2 * l) * kv_layer;
+      c.pre.v = (const __nv_bfloat16*)ctx->prefix_kv + (size_t)(2 * l + 1) * kv_layer;
+      c.pre.st = D;
+      c.pre.sh = (long long)k.max_prefix_len * D;
+      c.pre.len = P;
+      c.own.k = fp->ksb;
+      c.own.v = fp->vsb;
+      c.own.st = D;
+      c.own.sh = (long long)S * D;
+      c.own.sb = c.own.sh * k.n_kv_heads;
+      c.own.len = S;
+      c.status = ctx->status;
+      c.timeout_ns = k.barrier_timeout_ns;
+      if (e == cudaSuccess) e = run_attention(c, fp->num_sms, fp->att_po, fp->att_po_bytes, st);
     } else {
       at.trace = tr(l, 4);
       at.pk = (const __nv_bfloat16*)ctx->prefix_kv + (size_t)(2 * l) * kv_layer;
@@ -2708,8 +2771,9 @@ rtv_status layers_impl(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, cons
 }  // namespace
 
 rtv_status fast_layers(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, const float* rope_cs,
-                       const float* rope_sn, cudaStream_t st, const ModTables* mod, const FoldedQueries* fold) {
-  return layers_impl(ctx, G, P, prefix_batch_stride, rope_cs, rope_sn, st, mod, fold, false);
+                       const float* rope_sn, cudaStream_t st, const ModTables* mod, const FoldedQueries* fold,
+                       bool one_prefix) {
+  return layers_impl(ctx, G, P, prefix_batch_stride, rope_cs, rope_sn, st, mod, fold, false, one_prefix);
 }
 
 void folded_sizes(const rtv_ctx* ctx, int G, size_t bytes[4]) {

@@ -161,7 +161,8 @@ void time_condition(rtv_ctx* ctx, const float* taus, int n, int n_steps, float* 
   launch_linear<WT>(ctx->z_tmp, w, (const WT*)ctx->W.to_w, ctx->W.to_b, c, w, n, w, w, EPI_STORE, st);
 }
 
-enum { KIND_DENOISE = 0, KIND_VERIFY = 1 };
+// KIND_SHARED: denoising of several chunks over the prefix (and state) of batch element 0.
+enum { KIND_DENOISE = 0, KIND_VERIFY = 1, KIND_SHARED = 2 };
 
 // Precompute the input-independent tables of a graph (time condition of the
 // Euler schedule, RoPE table of the suffix positions, the time modulator's
@@ -174,6 +175,8 @@ rtv_status build_graph(rtv_ctx* ctx, int kind, int n, int batch, int P, GraphEnt
   const int S = ctx->S, D = k.head_dim, w = k.width, L = k.n_layers;
   const int nq = ctx->Q + 2 * ctx->KV, F2 = 2 * k.mlp_dim;
   const int tc = k.time_cond;
+  const bool shared = kind == KIND_SHARED, denoise = kind != KIND_VERIFY;
+  const int pbs = shared ? 0 : 1, state_gs = shared ? 0 : k.state_dim;   // group strides of the prefix batch and the state
   auto table = [&](float** p, size_t count) -> rtv_status {
     CK(cudaMalloc(p, sizeof(float) * count));
     ge.owned.push_back(*p);
@@ -183,7 +186,7 @@ rtv_status build_graph(rtv_ctx* ctx, int kind, int n, int batch, int P, GraphEnt
   TRY(table(&cs, (size_t)S * (D / 2)));
   TRY(table(&sn, (size_t)S * (D / 2)));
   launch_rope_table(cs, sn, S, D, P, k.rope_theta, st);
-  if (kind == KIND_DENOISE) {
+  if (denoise) {
     // per Euler step t_k (n <= 64 rows): c(t_k) = W_to swish(W_ti e(t_k) + b_ti) + b_to; with Pi0's
     // concat MLP instead the time half of its first layer, W_ti[:, w:] e(t_k) + b_ti; with the per-layer
     // modulator also the modulation rows of every layer
@@ -209,8 +212,8 @@ rtv_status build_graph(rtv_ctx* ctx, int kind, int n, int batch, int P, GraphEnt
   CK(cudaStreamSynchronize(st));
   // The resident kernel serves the plain time condition on the tensor-core
   // path when its plan fits (prepared here, outside the capture).
-  const bool use_res = ctx->use_fast && tc == RTV_TIME_ADD &&
-                       resident_prepare(ctx, kind == KIND_DENOISE ? batch : n, P, kind == KIND_VERIFY);
+  const bool use_res = ctx->use_fast && tc == RTV_TIME_ADD && !shared &&
+                       resident_prepare(ctx, denoise ? batch : n, P, kind == KIND_VERIFY);
 
   if (ctx->use_fast) fast_arm_trace(ctx);
   CK(cudaStreamBeginCapture(st, cudaStreamCaptureModeThreadLocal));
@@ -221,7 +224,7 @@ rtv_status build_graph(rtv_ctx* ctx, int kind, int n, int batch, int P, GraphEnt
   if (prologue) chain((*prologue)(st));
   // what the embedding of a step adds to the action rows: c (RTV_TIME_ADD) or nothing
   const bool add_c = tc == RTV_TIME_ADD;
-  if (kind == KIND_DENOISE) {
+  if (denoise) {
     const float dt = (float)(1.0 / (double)n);
     auto mod_of = [&](int step) {
       ModTables m;
@@ -242,23 +245,24 @@ rtv_status build_graph(rtv_ctx* ctx, int kind, int n, int batch, int P, GraphEnt
         }
       };
       const float* g00 = tc == RTV_TIME_ADARMS ? modtab : nullptr;
-      chain(fast_step(ctx, batch, false, true, dt, add_c ? ctab : ctx->czero, 0, k.state_dim, false, st, g00, 0));
+      chain(fast_step(ctx, batch, false, true, dt, add_c ? ctab : ctx->czero, 0, state_gs, false, st, g00, 0));
       embed_tail(0);
       for (int step = 0; step < n && fs == RTV_OK; ++step) {
         ModTables m;
         if (tc == RTV_TIME_ADARMS) m = mod_of(step);
-        chain(fast_layers(ctx, batch, P, 1, cs, sn, st, tc == RTV_TIME_ADARMS ? &m : nullptr));
+        chain(fast_layers(ctx, batch, P, pbs, cs, sn, st, tc == RTV_TIME_ADARMS ? &m : nullptr, nullptr,
+                          shared && k.suffix_mask == RTV_MASK_BIDIR));
         const bool more = step + 1 < n;
         const float* cnext = add_c ? (more ? ctab + (size_t)(step + 1) * w : ctab) : ctx->czero;
         const float* g0 = (tc == RTV_TIME_ADARMS && more) ? modtab + (size_t)(step + 1) * L * 6 * w : nullptr;
-        chain(fast_step(ctx, batch, true, more, dt, cnext, 0, k.state_dim, false, st, g0, 0));
+        chain(fast_step(ctx, batch, true, more, dt, cnext, 0, state_gs, false, st, g0, 0));
         if (more) embed_tail(step + 1);
       }
     } else {
       for (int step = 0; step < n; ++step) {
         ModTables m;
         if (tc == RTV_TIME_ADARMS) m = mod_of(step);
-        simt_expert<WT>(ctx, batch, P, add_c ? ctab + (size_t)step * w : ctx->czero, 0, k.state_dim, 1, cs, sn, st,
+        simt_expert<WT>(ctx, batch, P, add_c ? ctab + (size_t)step * w : ctx->czero, 0, state_gs, pbs, cs, sn, st,
                         tc == RTV_TIME_CONCAT ? ctab + (size_t)step * w : nullptr, 0,
                         tc == RTV_TIME_ADARMS ? &m : nullptr);
         launch_out_head<WT>(ctx->h, ctx->W.g_final, (const WT*)ctx->W.ao_w, ctx->W.ao_b, ctx->x, nullptr, dt, batch,
@@ -649,6 +653,26 @@ rtv_status rtv_denoise(rtv_ctx* ctx, const float* noise, const float* state, int
     fast_trace_report(ctx);
     resident_trace_report(ctx);
   }
+  return RTV_OK;
+}
+
+rtv_status rtv_denoise_shared(rtv_ctx* ctx, const float* noise, const float* state, int n_chunks, int n_steps,
+                              float* actions_out, rtv_stream stream) {
+  if (!ctx) return RTV_ERR_ARG;
+  if (!noise || !state || !actions_out) return fail(ctx, RTV_ERR_ARG, "null pointer");
+  if (!ctx->loaded || !ctx->have_prefix) return fail(ctx, RTV_ERR_STATE, "load the expert and the prefix first");
+  if (n_steps <= 0 || n_steps > 64) return fail(ctx, RTV_ERR_SHAPE, "n_steps must be in [1, 64]");
+  const rtv_expert_config& k = ctx->cfg;
+  if (n_chunks <= 0 || n_chunks > k.max_batch) return fail(ctx, RTV_ERR_SHAPE, "n_chunks must be in [1, max_batch]");
+  DeviceGuard dg(ctx->device);
+  cudaStream_t st = (cudaStream_t)stream;
+  GraphEntry* ge = nullptr;
+  TRY(get_graph(ctx, KIND_SHARED, n_steps, n_chunks, &ge));
+  const size_t xb = (size_t)n_chunks * ctx->H * k.action_dim * sizeof(float);
+  CK(cudaMemcpyAsync(ctx->x, noise, xb, cudaMemcpyDefault, st));
+  CK(cudaMemcpyAsync(ctx->state, state, (size_t)k.state_dim * sizeof(float), cudaMemcpyDefault, st));
+  CK(cudaGraphLaunch(ge->exec, st));
+  CK(cudaMemcpyAsync(actions_out, ctx->x, xb, cudaMemcpyDefault, st));
   return RTV_OK;
 }
 

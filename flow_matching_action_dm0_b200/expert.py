@@ -4,6 +4,9 @@
     ex.load(weights)                         # rtv_load_expert
     ex.set_prefix_kv(kv)                     # rtv_set_prefix_kv
     chunk = ex.denoise(noise, state, 10)     # rtv_denoise
+    chunks = ex.denoise_shared(noises, state, 10)          # rtv_denoise_shared: candidates of one observation
+    parked = ex.get_prefix_kv_quantized(prefix_len)        # rtv_get_prefix_kv_quantized (E4M3 codes and scales)
+    ex.set_prefix_kv_quantized(*parked)                    # rtv_set_prefix_kv_quantized
     acc, flags, dist = ex.verify(draft, eps, state, taus, delta, gripper_dim)   # rtv_verify
 
 ``shape`` is any object with the rtv_expert_config field names (n_layers,
@@ -159,6 +162,49 @@ class ActionExpert:
         if isinstance(out, np.ndarray):
             self.synchronize(stream)
         return out
+
+    def denoise_shared(self, noise, state, n_steps: int, out=None, stream=None):
+        """Candidate chunks [n][H][A] fp32 of the observation of batch element
+        0, from noise [n][H][A] and one state [Sd].  numpy or torch fp32."""
+        if out is None:
+            if isinstance(noise, np.ndarray):
+                out = np.empty_like(noise, dtype=np.float32)
+            else:
+                out = noise.new_empty(noise.shape)
+        pn, _ = _ptr(noise)
+        ps, _ = _ptr(state)
+        po, _ = _ptr(out)
+        L.rtv_denoise_shared(self.h, pn, ps, int(noise.shape[0]), int(n_steps), po, _stream(stream))
+        if isinstance(out, np.ndarray):
+            self.synchronize(stream)
+        return out
+
+    def get_prefix_kv_quantized(self, prefix_len: int, batch: int = 1, stream=None):
+        """The installed prefix (of that length and batch) in E4M3: codes
+        [L][2][B][Hkv][P][D] (torch.float8_e4m3fn) and scales [L][2][B][Hkv][P]
+        fp32, on the context's GPU."""
+        import torch
+        dev = torch.device("cuda", self.device)
+        shape = (self.cfg.n_layers, 2, int(batch), self.cfg.n_kv_heads, int(prefix_len))
+        codes = torch.empty(shape + (self.cfg.head_dim,), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        L.rtv_get_prefix_kv_quantized(self.h, codes.data_ptr(), scales.data_ptr(), int(prefix_len), int(batch),
+                                      _stream(stream))
+        return codes, scales
+
+    def set_prefix_kv_quantized(self, codes, scales, stream=None):
+        """Install what get_prefix_kv_quantized gave."""
+        if codes.shape[:-1] != scales.shape or tuple(codes.shape[:2]) != (self.cfg.n_layers, 2) or \
+                tuple(codes.shape[3::2]) != (self.cfg.n_kv_heads, self.cfg.head_dim):
+            raise ValueError("codes [L][2][B][Hkv][P][D] and scales [L][2][B][Hkv][P] expected")
+        if not str(codes.dtype).endswith(("float8_e4m3fn", "uint8")) or str(scales.dtype) != "torch.float32":
+            raise TypeError("E4M3 codes and fp32 scales expected")
+        pc, _ = _ptr(codes)
+        ps, _ = _ptr(scales)
+        self._keep = [codes, scales]
+        L.rtv_set_prefix_kv_quantized(self.h, pc, ps, int(codes.shape[4]), int(codes.shape[2]), _stream(stream))
 
     def verify(self, draft, noise, state, taus: Sequence[float], delta: float, gripper_dim: int,
                want_dist: bool = True, stream=None):

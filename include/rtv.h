@@ -201,6 +201,34 @@ rtv_status rtv_set_prefix_kv_static(rtv_ctx* ctx, const void* kv, int prefix_len
 rtv_status rtv_denoise(rtv_ctx* ctx, const float* noise, const float* state, int n_steps,
                        float* actions_out, rtv_stream stream);
 
+/* Denoise several candidate chunks of one observation: as rtv_denoise, for
+ * n_chunks noises [n_chunks][H][A] that share the prefix of batch element 0
+ * and one state [Sd], without a copy of the prefix for each.  actions_out is
+ * [n_chunks][H][A]; n_chunks <= max_batch.  The tensor-core path with the
+ * bidirectional mask reads the prefix through the shared-prefix attention
+ * (rtv_shared_attention's kernels); results agree with rtv_denoise's on
+ * copied prefixes to the paths' rounding.  Graphs, pointers and errors as
+ * for rtv_denoise. */
+rtv_status rtv_denoise_shared(rtv_ctx* ctx, const float* noise, const float* state, int n_chunks, int n_steps,
+                              float* actions_out, rtv_stream stream);
+
+/* Park the installed prefix in E4M3 (for example after rtv_prefill_kv, to
+ * serve another observation meanwhile): codes [n_layers][2][batch]
+ * [n_kv_heads][prefix_len][head_dim] and scales [n_layers][2][batch]
+ * [n_kv_heads][prefix_len] fp32, as rtv_kv_write makes them; half the bytes
+ * of a bf16 prefix.  prefix_len and batch must be the installed ones
+ * (RTV_ERR_SHAPE).  Device memory of the context's GPU, 16-byte aligned.
+ * head_dim 64, 128 or 256, otherwise RTV_ERR_UNSUPPORTED; RTV_ERR_STATE
+ * without a prefix. */
+rtv_status rtv_get_prefix_kv_quantized(rtv_ctx* ctx, void* codes, float* scales, int prefix_len, int batch,
+                                       rtv_stream stream);
+
+/* Install a parked prefix: the values code * scale, as rtv_kv_read gives
+ * them, in the layout above.  Otherwise as rtv_set_prefix_kv, with device
+ * memory only and no allocation. */
+rtv_status rtv_set_prefix_kv_quantized(rtv_ctx* ctx, const void* codes, const float* scales, int prefix_len, int batch,
+                                       rtv_stream stream);
+
 /* FLASH verification ([FLASH] 02, 03.2, 03.3) of one draft chunk against
  * the prefix of batch element 0: for each tau_i (host array of n_taus
  * values in [0,1]) form X_i = tau_i*noise + (1-tau_i)*draft, evaluate the
@@ -337,11 +365,12 @@ void rtv_draft_destroy(rtv_draft* d);
  * Layer l's keys (after RoPE) and values become the expert's cached prefix
  * of layer l, so the stack has the expert's n_layers, n_kv_heads and
  * head_dim.  The last layer's attention output and MLP are not computed.
+ * Past 960 tokens the attention is rtv_cross_attention's.
  * bf16 only (tensor-core path).
  * ------------------------------------------------------------------------ */
 typedef struct {
   int n_layers, width, n_q_heads, n_kv_heads, head_dim, mlp_dim;
-  int max_tokens;     /* largest n_tokens a call may pass (<= 960)                */
+  int max_tokens;     /* largest n_tokens a call may pass                         */
   int dtype;          /* RTV_BF16                                                 */
   float rms_eps;
   float rope_theta;   /* 0 disables rotary embedding                              */

@@ -131,3 +131,10 @@ def test_cache_operators_refuse_host_tensors_and_types_before_the_library():
         ops.cross_attention(x[0], (x, x))
     with pytest.raises(ValueError):
         ops.shared_attention(x, (x[0], x[0]), own_lens=x)
+
+
+def test_prefix_store_calls_are_refused_without_a_context():
+    lib = L.load_library()
+    assert lib.rtv_denoise_shared(None, None, None, 1, 1, None, None) == L.RTV_ERR_ARG
+    assert lib.rtv_get_prefix_kv_quantized(None, None, None, 1, 1, None) == L.RTV_ERR_ARG
+    assert lib.rtv_set_prefix_kv_quantized(None, None, None, 1, 1, None) == L.RTV_ERR_ARG
