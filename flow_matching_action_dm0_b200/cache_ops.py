@@ -14,7 +14,8 @@ of any strides with a dense last index and 16-byte steps.  Results are new
 tensors unless ``out`` is given.  Work goes to ``stream`` (a torch stream or
 its address), or to torch's current stream of the handle's GPU; results and
 workspaces are allocated for the stream that the work goes to, as if the call
-were made inside ``torch.cuda.stream(stream)``.
+were made inside ``torch.cuda.stream(stream)``.  Outputs must not overlap
+inputs, and no gradient flows through the calls.
 """
 
 from __future__ import annotations
@@ -28,6 +29,13 @@ from ._lib import RTV_BF16, RTV_F32, RTV_FP8_E4M3, rtv_kv, rtv_queries
 
 _CODES = {torch.float32: RTV_F32, torch.bfloat16: RTV_BF16}
 _TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _place(x, what: str) -> int:
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:   # (the C call takes an int; it refuses the negative ones)
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
 
 
 class QuantizedKV(NamedTuple):
@@ -72,7 +80,10 @@ class CacheOps:
     # ------------------------------------------------------------------
     def _on(self, stream):
         """Context in which torch allocates for, and names, the call's stream."""
-        if not isinstance(stream, torch.cuda.Stream):
+        if isinstance(stream, torch.cuda.Stream):
+            if stream.device_index != self.device:
+                raise ValueError(f"stream: of cuda:{stream.device_index}, not the handle's GPU (cuda:{self.device})")
+        else:
             stream = torch.cuda.ExternalStream(int(stream), device=self._torch_device) if stream else \
                 torch.cuda.default_stream(self._torch_device)
         return torch.cuda.stream(stream)
@@ -202,7 +213,7 @@ class CacheOps:
         if isinstance(start, torch.Tensor):
             at = self._ints(start, "start", src.batch)
         elif start is not None:
-            first = int(start)
+            first = _place(start, "start")
         L.rtv_kv_write(self.h, src, dst, at, first, self._ints(count, "count", src.batch), self._stream())
 
     def read(self, cache: QuantizedKV, n: Optional[int] = None, first: int = 0, lens=None, dtype="bf16", out=None,
@@ -213,7 +224,7 @@ class CacheOps:
         if stream is not None:
             with self._on(stream):
                 return self.read(cache, n, first, lens, dtype, out)
-        src = self._cache(cache, "cache")
+        src, first = self._cache(cache, "cache"), _place(first, "first")
         if out is None:
             n = src.n_tokens - first if n is None else n
             if n < 0 or dtype not in _TYPES:
@@ -221,6 +232,8 @@ class CacheOps:
             kv = torch.empty((2, src.batch, n, src.n_heads, src.head_dim), dtype=_TYPES[dtype],
                              device=self._torch_device)
             out = (kv[0], kv[1])
+        elif n is not None and n != out[0].shape[1]:
+            raise ValueError(f"read: n is {n}, out holds {out[0].shape[1]} tokens")
         dst = self._rows(out[0], out[1], "out")
         L.rtv_kv_read(self.h, src, first, self._ints(lens, "lens", src.batch), dst, self._stream())
         return out

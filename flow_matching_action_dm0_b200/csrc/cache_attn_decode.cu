@@ -14,9 +14,11 @@
 // E4M3 codes become f16 (exactly, one conversion for two) and so do the
 // queries, each row times a power of two that brings its largest magnitude to
 // 2^14 (what is lost is below 2^-38 of it).  Their products with P are in
-// units of 2^mv, mv the running maximum of score + log2(value scale), so that
-// f16 weights hold what matters whatever the scales; the row's sum keeps the
-// maximum m of the scores alone, and O is brought to it at the end.
+// units of 2^(mv - 7), mv the running maximum of score + log2(value scale):
+// f16 weights (2^15 at most) hold what matters whatever the scales, 2^-11 of
+// each down to 2^-21 of the largest and 2^-32 of the largest below it.  The
+// row's sum keeps the maximum m of the scores alone, and O is brought to it at
+// the end.
 // A group takes 16 keys of a tile with a running maximum of its own (raised,
 // and O rescaled, when it has grown by more than 8 in base 2); at head_dim
 // 256 it is two warps, each with half of the dims, that add their scores.
@@ -33,6 +35,7 @@ namespace {
 
 constexpr int kRows = 16;
 constexpr float kLazy = 8.f;
+constexpr float kUp = 7.f;                        // E4M3: weights count in units of 2^(mv - kUp); kUp + kLazy < 16 (f16's range)
 
 template <int D, bool F8>
 struct Cfg {
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
 #pragma unroll
   for (int j = 0; j < NI * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows n and n + 8
-  float mv[2] = {-INFINITY, -INFINITY};             // E4M3: O counts in units of 2^mv (bf16: of 2^m)
+  float mv[2] = {-INFINITY, -INFINITY};             // E4M3: O counts in units of 2^(mv - kUp) (bf16: of 2^m)
   const float scale = c.scale_log2;
   int slot = 0;
   for (int tile = u.t0; tile < u.t1; ++tile) {
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
       float w[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float b = m[r] == -INFINITY ? 0.f : m[r], bv = mv[r] == -INFINITY ? 0.f : mv[r];
+        const float b = m[r] == -INFINITY ? 0.f : m[r], bv = mv[r] == -INFINITY ? 0.f : mv[r] - kUp;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     const int row = n + 8 * r;
     if (F8) {
-      const float f = mv[r] == m[r] ? 1.f : ex2(mv[r] - m[r]);
+      const float f = m[r] == -INFINITY ? 1.f : ex2(mv[r] - kUp - m[r]);
 #pragma unroll
       for (int j = 0; j < NI * 8; ++j) {
         o[j][2 * r] *= f;

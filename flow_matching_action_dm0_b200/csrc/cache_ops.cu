@@ -60,18 +60,32 @@ rtv_status check_ptr(rtv_ops* h, const void* p, const char* what, uintptr_t alig
     if (_s != RTV_OK) return _s;         \
   } while (0)
 
+// Whether the rows of `inner` elements of an array that is written may share
+// elements: each stride, from the smallest, has to step over all that the
+// smaller ones reach.
+bool overlaps(long long inner, const int (&n)[3], const long long (&s)[3]) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return s[a] < s[b]; });
+  long long reach = inner;
+  for (const int i : order) {
+    if (n[i] <= 1) continue;
+    if (s[i] < reach) return true;
+    if (s[i] > (1LL << 62) / n[i]) return false;   // (nothing allocated is that long; the rest steps further)
+    reach = std::max(reach, s[i] * (n[i] - 1) + reach);
+  }
+  return false;
+}
+
 // Strides of an array with a dense head_dim: multiples of 16 bytes, not
-// negative, and not 0 over an index that is written.
-rtv_status check_strides(rtv_ops* h, const char* what, long long eb, bool written, int n0, long long s0, int n1,
+// negative, and of rows that do not overlap when they are written.
+rtv_status check_strides(rtv_ops* h, const char* what, long long eb, bool written, int dim, int n0, long long s0, int n1,
                          long long s1, int n2, long long s2) {
   const int n[3] = {n0, n1, n2};
   const long long s[3] = {s0, s1, s2};
-  for (int i = 0; i < 3; ++i) {
-    if (n[i] <= 1) continue;
-    if (s[i] < 0 || (s[i] * eb) % 16 || s[i] > (1LL << 39) / eb)
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] < 0 || (s[i] * eb) % 16 || s[i] > (1LL << 39) / eb))
       return ofail(h, RTV_ERR_ARG, std::string(what) + ": strides must be multiples of 16 bytes, from 0 to 2^39");
-    if (written && s[i] == 0) return ofail(h, RTV_ERR_ARG, std::string(what) + ": stride 0 over an index that is written");
-  }
+  if (written && overlaps(dim, n, s)) return ofail(h, RTV_ERR_ARG, std::string(what) + ": rows that are written overlap");
   return RTV_OK;
 }
 
@@ -95,21 +109,18 @@ rtv_status check_kv_shape(rtv_ops* h, const rtv_kv* a, const char* what) {
 rtv_status check_kv_memory(rtv_ops* h, const rtv_kv* a, const std::string& what, bool written) {
   OTRY(check_ptr(h, a->k, (what + " k").c_str(), 16));
   OTRY(check_ptr(h, a->v, (what + " v").c_str(), 16));
-  OTRY(check_strides(h, what.c_str(), elt_bytes(a->dtype), written, a->batch, a->batch_stride, a->n_tokens,
+  OTRY(check_strides(h, what.c_str(), elt_bytes(a->dtype), written, a->head_dim, a->batch, a->batch_stride, a->n_tokens,
                      a->token_stride, a->n_heads, a->head_stride));
-  if (a->dtype != RTV_FP8_E4M3) {
-    // rows of one call's source may be shared between elements and heads, not between tokens
-    if (a->n_tokens > 1 && a->token_stride == 0) return ofail(h, RTV_ERR_ARG, what + ": token stride 0");
-    return RTV_OK;
-  }
+  // rows of one call's source may be shared between elements and heads, not between tokens
   if (a->n_tokens > 1 && a->token_stride == 0) return ofail(h, RTV_ERR_ARG, what + ": token stride 0");
+  if (a->dtype != RTV_FP8_E4M3) return RTV_OK;
   OTRY(check_ptr(h, a->k_scale, (what + " k_scale").c_str(), 4));
   OTRY(check_ptr(h, a->v_scale, (what + " v_scale").c_str(), 4));
   const int n[3] = {a->batch, a->n_tokens, a->n_heads};
   const long long s[3] = {a->scale_batch_stride, a->scale_token_stride, a->scale_head_stride};
   for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && (s[i] < 0 || s[i] > (1LL << 39) || (written && s[i] == 0)))
-      return ofail(h, RTV_ERR_ARG, what + ": bad scale stride");
+    if (n[i] > 1 && (s[i] < 0 || s[i] > (1LL << 39))) return ofail(h, RTV_ERR_ARG, what + ": bad scale stride");
+  if (written && overlaps(1, n, s)) return ofail(h, RTV_ERR_ARG, what + ": scales that are written overlap");
   return RTV_OK;
 }
 
@@ -206,8 +217,8 @@ rtv_status attention(rtv_ops* h, const rtv_queries* q, const rtv_kv* pre, const 
   OTRY(check_ptr(h, q->q, "q", 16));
   OTRY(check_ptr(h, q->out, "out", 16));
   const long long eb = elt_bytes(q->dtype);
-  OTRY(check_strides(h, "q", eb, false, c.B, q->q_batch_stride, c.Tq, q->q_token_stride, c.Hq, q->q_head_stride));
-  OTRY(check_strides(h, "out", eb, true, c.B, q->out_batch_stride, c.Tq, q->out_token_stride, c.Hq, q->out_head_stride));
+  OTRY(check_strides(h, "q", eb, false, c.D, c.B, q->q_batch_stride, c.Tq, q->q_token_stride, c.Hq, q->q_head_stride));
+  OTRY(check_strides(h, "out", eb, true, c.D, c.B, q->out_batch_stride, c.Tq, q->out_token_stride, c.Hq, q->out_head_stride));
   if (q->lse) OTRY(check_ptr(h, q->lse, "lse", 4));
   auto source = [&](const rtv_kv* a, const char* what, const int* l, const unsigned char* m, long long ms, KvSource* s) -> rtv_status {
     if (!a || a->n_tokens == 0) return RTV_OK;

@@ -166,6 +166,11 @@ class ActionExpert:
     def denoise_shared(self, noise, state, n_steps: int, out=None, stream=None):
         """Candidate chunks [n][H][A] fp32 of the observation of batch element
         0, from noise [n][H][A] and one state [Sd].  numpy or torch fp32."""
+        chunk = (self.cfg.chunk_len, self.cfg.action_dim)
+        if tuple(noise.shape[1:]) != chunk or tuple(state.shape) not in ((self.cfg.state_dim,), (1, self.cfg.state_dim)):
+            raise ValueError(f"noise [n]{list(chunk)} and state [{self.cfg.state_dim}] expected")
+        if out is not None and tuple(out.shape) != tuple(noise.shape):
+            raise ValueError("out: the noise's shape expected")
         if out is None:
             if isinstance(noise, np.ndarray):
                 out = np.empty_like(noise, dtype=np.float32)

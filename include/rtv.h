@@ -441,7 +441,10 @@ void rtv_prefill_destroy(rtv_prefill* p);
  * nothing and keep nothing between them, so they may be captured into a
  * CUDA graph and run on several streams at once, as long as each has a
  * workspace of its own; calls on one handle must not run concurrently from
- * several host threads.  Outputs must not overlap inputs.
+ * several host threads, and a captured call is not replayed after
+ * rtv_ops_destroy.  Outputs must not overlap inputs, nor the rows of an
+ * output each other (RTV_ERR_ARG unless each stride steps over all that the
+ * smaller ones reach).
  * ------------------------------------------------------------------------ */
 typedef struct rtv_ops rtv_ops;
 
@@ -467,9 +470,9 @@ typedef struct {
  * Queries and where their attention goes: q and out [batch][n_tokens]
  * [n_heads][head_dim] in dtype (RTV_F32 or RTV_BF16); lse, when not NULL, is
  * dense [batch][n_tokens][n_heads] fp32: the natural logarithm of the sum of
- * exp(score).  score = scale * q.k, scale finite and not 0.  n_heads is a multiple of the keys'
- * heads; query head h reads key/value head h / (n_heads / kv heads).  A query
- * that sees no key gives out = 0 and lse = -infinity.
+ * exp(score).  score = scale * q.k, scale finite and not 0.  n_heads is a
+ * multiple of the keys' heads; query head h reads key/value head h / (n_heads
+ * / kv heads).  A query that sees no key gives out = 0 and lse = -infinity.
  */
 typedef struct {
   const void* q;
@@ -502,8 +505,8 @@ rtv_status rtv_kv_write(rtv_ops* ops, const rtv_kv* src, const rtv_kv* cache, co
                         const int* count, rtv_stream stream);
 
 /* Read cache tokens first .. first + dst->n_tokens - 1 of every element into
- * dst (RTV_F32 or RTV_BF16): code * scale, rounded once to dst's dtype (exact
- * in bf16 when the scale is a power of two).  Tokens at or past lens[b]
+ * dst (RTV_F32 or RTV_BF16): code * scale in fp32, rounded to dst's dtype
+ * (exact in both when the scale is a power of two).  Tokens at or past lens[b]
  * (device int32 [batch], or NULL) read as zeros; so do those that a length
  * outside [0, cache tokens] cannot mean (it is clamped, RTV_DEV_BOUNDS). */
 rtv_status rtv_kv_read(rtv_ops* ops, const rtv_kv* cache, int first, const int* lens, const rtv_kv* dst,
@@ -516,7 +519,12 @@ rtv_status rtv_kv_read(rtv_ops* ops, const rtv_kv* cache, int first, const int* 
  * in the queries' dtype or RTV_FP8_E4M3.  What hidden keys and values hold is
  * never used, NaN and infinities included.  bf16 queries: products on the
  * tensor cores with fp32 sums, softmax weights rounded to bf16; fp32 queries:
- * fp32 throughout.  workspace: at least rtv_cross_attention_workspace bytes,
+ * fp32 throughout.  bf16 queries over E4M3: up to 16 rows (query tokens x
+ * query heads of a key/value head) take the codes as they are, with weight x
+ * value scale rounded to f16 (2^-11 of each, and 2^-32 of the row's largest);
+ * more rows, and a prefix that several elements share or that has own keys
+ * beside it, are read back to bf16 in the workspace first, so it grows with
+ * the cache.  workspace: at least rtv_cross_attention_workspace bytes,
  * 256-byte aligned (NULL when that is 0), in use until the call's work is
  * done. */
 rtv_status rtv_cross_attention(rtv_ops* ops, const rtv_queries* q, const rtv_kv* kv, const int* lens,

@@ -548,3 +548,56 @@ def test_host_pointers_are_refused_before_anything_runs(ops):
     for q, k in ((qs(host, dev), kv(dev)), (qs(dev, host), kv(dev)), (qs(dev, dev), kv(host))):
         assert lib.rtv_cross_attention(ops.h, C.byref(q), C.byref(k), None, None, 0, None, 0, None) == L.RTV_ERR_ARG
         assert b"GPU" in lib.rtv_ops_last_error(ops.h) or b"device" in lib.rtv_ops_last_error(ops.h)
+
+
+@pytest.mark.parametrize("b,tq,d", [(1, 1, 64), (2, 3, 128), (1, 2, 256), (2, 30, 64)])
+def test_value_rows_of_very_different_sizes(ops, b, tq, d):
+    """Every other key's values are 2^17 times the others', in dims of their own: the small ones still count in
+    theirs, to the weights' step."""
+    g = gen(31 + d)
+    n, half = 40, d // 2
+    q, k = rand(g, b, tq, 4, d, size=0.1), rand(g, b, n, 1, d)
+    v = rand(g, b, n, 1, d)
+    v[:, 0::2, :, half:] = 0
+    v[:, 1::2, :, :half] = 0
+    v[:, 0::2] *= 2.0 ** 9
+    v[:, 1::2] *= 2.0 ** -8
+    cache = empty_cache(b, n, 1, d)
+    ops.write(cache, k, v)
+    kr, vr = (f64(x) for x in ops.read(cache, dtype="f32"))
+    out, lse = ops.cross_attention(q, cache, lse=True)
+    check_attention(q, lambda i: [(kr[i], vr[i], np.ones(n, bool))], d ** -0.5, out, lse)
+
+
+def test_outputs_whose_rows_overlap_are_refused(ops):
+    from flow_matching_action_dm0_b200 import QuantizedKV, RtvError
+    g = gen(32)
+    q, k, v = rand(g, 2, 3, 4, 64), rand(g, 2, 10, 2, 64), rand(g, 2, 10, 2, 64)
+    flat = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
+    for shape, stride in (((2, 3, 4, 64), (768, 64, 64, 1)), ((2, 3, 4, 64), (64, 256, 64, 1)), ((2, 3, 4, 64), (768, 256, 56, 1)),
+                          ((2, 3, 4, 64), (0, 256, 64, 1))):
+        with pytest.raises(RtvError) as e:
+            ops.cross_attention(q, (k, v), out=flat.as_strided(shape, stride))
+        assert e.value.status == 1
+    cache = empty_cache(2, 10, 2, 64)
+    with pytest.raises(RtvError) as e:
+        ops.write(QuantizedKV(cache.k, cache.v, cache.k_scale[:, :1].expand(2, 2, 10), cache.v_scale[:, :1].expand(2, 2, 10)), k, v)
+    assert e.value.status == 1
+    with pytest.raises(RtvError) as e:
+        ops.write(QuantizedKV(cache.k[:1].expand(2, 2, 10, 64), cache.v[:1].expand(2, 2, 10, 64), cache.k_scale, cache.v_scale), k, v)
+    assert e.value.status == 1
+    with pytest.raises(RtvError) as e:
+        ops.read(cache, out=(flat.as_strided((2, 10, 2, 64), (64, 128, 64, 1)),) * 2)
+    assert e.value.status == 1
+    assert not flat.any() and (cache.k_scale == 0).all()
+
+
+def test_places_and_sizes_that_do_not_fit_are_refused(ops):
+    g = gen(33)
+    k = rand(g, 1, 4, 1, 64)
+    cache = empty_cache(1, 8, 1, 64)
+    for call in (lambda: ops.write(cache, k, k, start=2 ** 32), lambda: ops.read(cache, n=1, first=2 ** 32),
+                 lambda: ops.read(cache, n=3, out=(k, k)), lambda: ops.read(cache, n=-1)):
+        with pytest.raises(ValueError):
+            call()
+    assert (cache.k_scale == 0).all()

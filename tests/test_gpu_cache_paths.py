@@ -174,3 +174,15 @@ def test_prefill_past_the_tiled_attention(cuda_ok, n_tokens):
     assert pf.status() == (0, 0) and ex.status() == (0, 0)
     pf.close()
     ex.close()
+
+
+def test_denoise_shared_shapes(cuda_ok):
+    cfg = get_config("tiny-fp32")
+    ex, W, kv = expert(cfg, 2)
+    noise, state = np.ascontiguousarray(make_noise(cfg, batch=2)), make_state(cfg)[0]
+    for bad in ((noise[:, 1:], state), (noise, state[1:]), (noise, np.zeros((2, cfg.state_dim), np.float32))):
+        with pytest.raises(ValueError):
+            ex.denoise_shared(np.ascontiguousarray(bad[0]), bad[1], 2)
+    with pytest.raises(ValueError):
+        ex.denoise_shared(noise, state, 2, out=np.zeros_like(noise[:1]))
+    ex.close()
