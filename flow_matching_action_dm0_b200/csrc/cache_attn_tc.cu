@@ -3,9 +3,9 @@
 // keys.
 //
 // A CTA takes up to 256 rows (query token x head of a KV head's group; 128 at
-// head_dim 256) against a range of 128-key tiles, in one pass over them:
-//   S = Q K^T    tcgen05, 128 x 128, K in chunks of 64 dims from a ring of
-//                16 KB stages filled by TMA                        -> TMEM
+// head_dim 256) against a range of key tiles, in one pass over them:
+//   S = Q K^T    tcgen05, 128 rows x 128 keys (64 at head_dim 256), K from a
+//                ring of 16 KB stages filled by TMA                 -> TMEM
 //   P = 2^(S - m) a thread per row, straight from TMEM; the row's sum is kept
 //                in fp32, P rounded to bf16 (the MMA's input type) and
 //                written over S in TMEM
@@ -22,9 +22,28 @@
 // on.  The MMA warp issues S(q + 1) before PV(q), so that the tensor cores
 // have work while a group exponentiates.  Warp 0 issues the loads, warp 1 the
 // MMAs, warps 4-11 are the groups.
+//
+// At head_dim 256 O takes half of the tensor memory.  Key tiles of 64 leave
+// room there for Q too, so that the ring has 14 stages instead of 10: three
+// and a half tiles of keys and values.  (A 64-key step takes 1.6-1.7 thousand
+// cycles, 1.1 thousand of them the tensor cores'; with 128-key tiles and Q in
+// shared memory two such steps' worth took 4.3 thousand.)
+//
+// Few units are split over key ranges.  Up to eight ranges of a unit form a
+// cluster, stage their rows in shared memory and join them there, each CTA a
+// share of the rows; more are joined by combine_kernel.
+//
+// What it reaches, and what bounds it (B200, cold L2): 2050 queries x 4001
+// keys x 4 elements at head_dim 128, 305-310 us, 870 TFLOP/s of the 1657 a
+// matrix product reaches: a step's chain S -> softmax -> P V, of which the
+// exponentials and their conversion are the longest part, fills the time of
+// two steps' products, and 528 CTAs on 148 SMs leave the last of four waves
+// 57% empty.  16 suffixes of 51 tokens x 8 heads at head_dim 256 over 816 keys: 20.5
+// us, launch 2.5, Q and the first tiles 3, tiles 6, join 5.
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache_ops.h"
 #include "common.cuh"
@@ -35,8 +54,9 @@ namespace rtv {
 namespace {
 
 constexpr int kStage = 16384;                    // a bf16 stage: 128 rows of 128 bytes
-constexpr int kTile = 128;                       // rows of a unit, keys of a tile
+constexpr int kTile = 128;                       // rows of a row tile
 constexpr float kLazy = 8.f;                     // growth of a maximum (base 2) that rescales O
+constexpr int kFirst = 2;                        // loads of the ring that go before Q has been read
 constexpr long long kDrainNs = 200000000LL;      // limit of the waits for what is in flight after a timeout
 
 // Tensor maps of the two sources' keys and values, and whether a source's
@@ -48,11 +68,18 @@ struct __align__(64) AttnMaps {
 
 template <int D>
 struct Cfg {
-  static constexpr int NC = D / 64;                       // stages of a K or V tile
+  static constexpr int DC = D / 64;                       // chunks of 64 dims
+  static constexpr int KT = attention_tc_keys(D);         // keys of a tile
+  static constexpr int CK = kStage / (KT * 128);          // chunks of a K stage
   static constexpr int VK = 8192 / D;                     // keys of a V stage
+  static constexpr int NC = DC / CK;                      // stages of a K or V tile
+  static_assert(NC * VK == KT, "as many V stages");
   static constexpr int MT = D == 256 ? 1 : 2;             // row tiles that fit the tensor memory
-  static constexpr int QB = kTile * D * 2;                // bytes of a Q tile
-  static constexpr int NST = 10;
+  static constexpr bool kQInTmem = D == 256;              // Q's place: tensor memory, or shared memory
+  static constexpr int QB = kQInTmem ? 0 : kTile * D * 2; // bytes of a Q tile in shared memory
+  static constexpr int NST = kQInTmem ? 14 : 10;
+  static constexpr int kO = 2 * KT, kQ = kO + D;          // tensor memory: two S buffers, O (128 columns a row tile of two), Q
+  static_assert(!kQInTmem || kQ + D / 2 <= 512, "tensor memory");
   static constexpr int kThreads = 384;
   static constexpr int kSoft = 4;                         // first softmax warp
   // Registers of a softmax thread (it holds a row of S) and of the others:
@@ -63,8 +90,9 @@ struct Cfg {
   static constexpr int kSmall = 512 + 512 + 64;           // barriers, maxima, visible keys
   static constexpr int kSmem = 1024 + kOff + kSmall;
   static constexpr int kRowBytes = D * 4 + 16;            // a staged output row
-  static_assert(MT * kTile * kRowBytes <= kOff, "output rows are staged where the tiles were");
-  static_assert(2 * NC <= NST, "V(j) and the next K are held at once");
+  static constexpr int kStaged = MT * kTile * kRowBytes;  // and behind them, for a cluster's join, maxima and sums
+  static_assert(kStaged + MT * kTile * 8 <= kOff, "output rows are staged where the tiles were");
+  static_assert(3 * NC <= NST, "V(j), the next K and the one behind it are held at once");
   static_assert(kSmem <= 232448 - 64, "shared memory of a CTA");
 };
 
@@ -193,17 +221,19 @@ struct TileAt {
   bool pre;
   int k0, nk;                                     // first key, keys of the tile
 };
+template <int KT>
 __device__ __forceinline__ TileAt tile_at(const AttnUnit& u, int t) {
   TileAt a;
   a.pre = t < u.n0;
-  a.k0 = (a.pre ? t : t - u.n0) * kTile;
-  a.nk = min(kTile, (a.pre ? u.len0 : u.len1) - a.k0);
+  a.k0 = (a.pre ? t : t - u.n0) * KT;
+  a.nk = min(KT, (a.pre ? u.len0 : u.len1) - a.k0);
   return a;
 }
 
 // The tile may hold hidden keys: its end, or a mask.
+template <int KT>
 __device__ __forceinline__ bool has_hidden(const AttnCall& c, const TileAt& t) {
-  return t.nk < kTile || (t.pre ? c.pre.mask : c.own.mask) != nullptr;
+  return t.nk < KT || (t.pre ? c.pre.mask : c.own.mask) != nullptr;
 }
 
 // Named barriers: 1 all softmax warps, 2 and 3 a softmax group, 4.. a pair of warps of the groups.
@@ -220,7 +250,7 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attn_cache_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnMaps maps) {
   using C = Cfg<D>;
-  constexpr int NC = C::NC, NST = C::NST, VK = C::VK;
+  constexpr int NC = C::NC, NST = C::NST, VK = C::VK, KT = C::KT;
   extern __shared__ uint8_t sm_raw[];
   __shared__ int s_abort;
   uint8_t* Qs = (uint8_t*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
@@ -229,12 +259,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   uint64_t* empty = ready + NST;                  // [NST] the stage's MMAs have completed
   uint64_t* s_full = empty + NST;                 // [2] S of a buffer is complete
   uint64_t* p_ready = s_full + 2;                 // [2] P of a buffer is written (and hidden values are zeroed)
-  uint64_t* v_landed = p_ready + 2;               // [2] the values of a step with hidden keys are in their stages
-  uint64_t* q_ready = v_landed + 2;               // [2] Q rows of a group
+  uint64_t* q_ready = p_ready + 2;                // [2] Q rows of a group
   uint64_t* pv_done = q_ready + 2;                // one row tile: O += P V of a step has completed
   uint64_t* o_done = pv_done + 1;                 // every MMA of the CTA has completed
   uint32_t* tslot = (uint32_t*)(o_done + 1);
-  static_assert((2 * NST + 10) * 8 + 8 <= 512, "barriers fit their space");
+  static_assert((2 * NST + 8) * 8 + 8 <= 512, "barriers fit their space");
   float* m_row = (float*)(Qs + C::kOff + 512);    // [128] the maximum that the groups hand on (one row tile)
   uint32_t* seen = (uint32_t*)(m_row + 128);      // [2 groups][4] visible keys of the group's tile
 
@@ -249,7 +278,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s_full[i], 1);
       ptx::mbar_init(&p_ready[i], 4);
-      ptx::mbar_init(&v_landed[i], 1);
       ptx::mbar_init(&q_ready[i], 4);
     }
     ptx::mbar_init(pv_done, 1);
@@ -270,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   ptx::pdl_launch_dependents();                   // (tensor memory is allocated; combine_kernel waits for this grid's end)
-  const uint32_t o_tmem = tmem + 2 * kTile;       // two S buffers, then O of each row tile
+  const uint32_t o_tmem = tmem + C::kO;
   // After a wait has run out every other one gives up at once, so that all
   // warps reach the end (and the barriers among them) without their data.
   auto wait = [&](uint64_t* bar, int parity) {
@@ -294,8 +322,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       bool ok = true;
       int s = 0, ph = 1;
       for (int i = 0; i < 2 * n && ok; ++i) {
+        if (C::kQInTmem && i == kFirst) {   // (Q passes through the ring's other stages)
+          ok = wait(&q_ready[0], 0);
+          ok = wait(&q_ready[1], 0) && ok;
+          if (!ok) break;
+        }
         const int o = order.at(i);
-        const TileAt t = tile_at(u, u.t0 + (o >> 1));
+        const TileAt t = tile_at<KT>(u, u.t0 + (o >> 1));
         const CUtensorMap* map = (o & 1) ? (t.pre ? &maps.pre_v : &maps.own_v) : (t.pre ? &maps.pre_k : &maps.own_k);
         const int h = t.pre ? pre_h : own_h, b = t.pre ? 0 : own_b;
 #pragma unroll
@@ -303,9 +336,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           ok = ok && wait(&empty[s], ph);
           if (!ok) break;
           ptx::mbar_expect_tx(&ready[s], (uint32_t)kStage);
-          // a K stage is a chunk of 64 dims of 128 keys, a V stage all dims of VK keys
+          // a K stage is CK chunks of 64 dims of the tile's keys, a V stage all dims of VK keys
           if (o & 1) tma_load(ring + s * kStage, map, t.k0 + cc * VK, 0, h, b, &ready[s]);
-          else tma_load(ring + s * kStage, map, t.k0, cc, h, b, &ready[s]);
+          else tma_load(ring + s * kStage, map, t.k0, cc * C::CK, h, b, &ready[s]);
           if (++s == NST) s = 0, ph ^= 1;
         }
       }
@@ -315,14 +348,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // ---- MMAs: the whole warp walks the steps, one lane issues -----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (n > 0) {
-      const uint32_t id_s = ptx::idesc_bf16_f32(128, kTile), id_o = ptx::idesc_bf16_f32(128, D) | kBTransposed;
+      const uint32_t id_s = ptx::idesc_bf16_f32(128, KT), id_o = ptx::idesc_bf16_f32(128, D) | kBTransposed;
       const uint64_t qd = ptx::sw128_kmajor_desc(ptx::smem_u32(Qs)), kd = ptx::sw128_kmajor_desc(ptx::smem_u32(ring));
       const uint64_t vd = sw128_mnmajor_desc(ptx::smem_u32(ring), VK * 128);
       const bool leader = elect_one();
-      // tiles with hidden keys, as has_hidden says
-      const bool pre_mask = c.pre.mask != nullptr, own_mask = c.own.mask != nullptr;
-      const int pre_end = u.len0 % kTile ? u.n0 - 1 - u.t0 : -1;            // key tiles (of the unit) that end early
-      const int own_end = u.len1 % kTile ? u.n0 + u.len1 / kTile - u.t0 : -1, own0 = u.n0 - u.t0;
       const uint32_t s_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32), q_lo = (uint32_t)qd, k_lo = (uint32_t)kd,
                      v_lo = (uint32_t)vd;
       bool ok = true;
@@ -334,29 +363,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (++s == NST) s = 0, ++ph;
         }
       };
-      // Where the ring holds the next K beside the K in use, loads are awaited
-      // ahead, so that a product and the next scores are issued in one run;
-      // otherwise each stage is awaited as its turn comes.
-      constexpr bool kAhead = 3 * NC <= NST;
-      auto stage_landed = [&](int s, int ph) {
-        if (kAhead) return;
-        ok = ok && wait(&ready[s], ph);
-        ptx::tc_fence_after();
-      };
       auto scores = [&](int q) {                  // S(q), over P(q - 2), whose MMA comes before it in this thread's order
         const int buf = q & 1, rt = two ? buf : 0, pos = order.of_k(two ? q >> 1 : q) * NC;
-        int s = pos % NST, ph = pos / NST;
+        int s = pos % NST;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
-          stage_landed(s, ph);
           if (leader && ok) {
             const uint32_t qa = q_lo + rt * (C::QB >> 4) + cc * (16384 >> 4), ka = k_lo + s * (kStage >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::umma_bf16(tmem + buf * kTile, desc64(qa + 2 * kk, s_hi), desc64(ka + 2 * kk, s_hi), id_s, (cc | kk) != 0);
+            for (int kk = 0; kk < 4 * C::CK; ++kk) {
+              const uint64_t kdesc = desc64(ka + (kk >> 2) * (KT * 128 >> 4) + 2 * (kk & 3), s_hi);
+              if (C::kQInTmem) umma_bf16_ts(tmem + buf * KT, tmem + C::kQ + cc * 32 * C::CK + 8 * kk, kdesc, id_s, (cc | kk) != 0);
+              else ptx::umma_bf16(tmem + buf * KT, desc64(qa + 2 * kk, s_hi), kdesc, id_s, (cc | kk) != 0);
+            }
             if (!two || rt == 1) ptx::umma_commit(&empty[s]);   // the key tile's last use
           }
-          if (++s == NST) s = 0, ++ph;
+          if (++s == NST) s = 0;
         }
         if (leader && ok) {
           ptx::umma_commit(&s_full[buf]);
@@ -364,12 +386,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       };
       ok = wait(&q_ready[0], 0);
       if (!two) ok = wait(&q_ready[1], 0) && ok;
-      if (kAhead) landed(order.of_k(0));
+      landed(order.of_k(0));
       ptx::tc_fence_after();
       scores(0);
       if (steps > 1) {
         if (two) ok = wait(&q_ready[1], 0) && ok;
-        else if (kAhead) landed(order.of_k(1));
+        else landed(order.of_k(1));
         ptx::tc_fence_after();
         scores(1);
       }
@@ -377,27 +399,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int buf = q & 1, rt = two ? buf : 0, j = two ? q >> 1 : q;
         const bool next = q + 2 < steps;
         if (rt == 0) {
-          const bool hidden = (j < own0 ? pre_mask : own_mask) || j == pre_end || j == own_end;
-          if (kAhead || hidden) landed(order.of_v(j));
-          if (hidden && leader && ok) ptx::mbar_arrive(&v_landed[buf]);
-          if (kAhead && next) landed(order.of_k(two ? j + 1 : q + 2));
+          landed(order.of_v(j));
+          if (next) landed(order.of_k(two ? j + 1 : q + 2));
         }
         ok = ok && wait(&p_ready[buf], q >> 1);
         ptx::tc_fence_after();
         const int pos = order.of_v(j) * NC;
-        int s = pos % NST, ph = pos / NST;
+        int s = pos % NST;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
-          stage_landed(s, ph);
           if (leader && ok) {
             const uint32_t va = v_lo + s * (kStage >> 4);
 #pragma unroll
             for (int kk = 0; kk < VK / 16; ++kk)
-              umma_bf16_ts(o_tmem + rt * kTile, tmem + buf * kTile + (cc * VK + kk * 16) / 2, desc64(va + kk * (2048 >> 4), v_hi),
+              umma_bf16_ts(o_tmem + rt * kTile, tmem + buf * KT + (cc * VK + kk * 16) / 2, desc64(va + kk * (2048 >> 4), v_hi),
                            id_o, (j | cc | kk) != 0);
             if (!two || rt == 1) ptx::umma_commit(&empty[s]);
           }
-          if (++s == NST) s = 0, ++ph;
+          if (++s == NST) s = 0;
         }
         if (leader && ok) {
           if (!two) ptx::umma_commit(pv_done);
@@ -425,11 +444,41 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const long long row = u.row0 + (mine ? tile_row + r : 0);
     const unsigned b = (unsigned)row / (unsigned)c.plan.rows_b, rr = (unsigned)row - b * (unsigned)c.plan.rows_b;
     const unsigned t_row = rr / (unsigned)c.group, h_row = u.kvh * c.group + rr - t_row * (unsigned)c.group;
-    // Q rows: the warp's own 32 (with one row tile the groups take 16 each), 16 bytes a lane
-    {
+    // Q rows, negated for a negative scale
+    const long long off = b * c.qb + (long long)t_row * c.qt + (long long)h_row * c.qh;
+    const uint32_t flip = c.scale_log2 < 0.f ? 0x80008000u : 0u;
+    if (C::kQInTmem) {   // a row a thread, half of its dims a group; whole rows are read, and turned where the ring is not yet in use
+      constexpr int CPR = D / 16, RPI = 32 / CPR, LD = D + 16;   // 16-byte chunks of half a row, rows of a warp's step, bytes of one
+      static_assert(kFirst * NC * kStage + 8 * 32 * LD <= NST * kStage, "the ring's rest holds Q");
+      uint8_t* at = ring + kFirst * NC * kStage + (warp - C::kSoft) * 32 * LD;
+      const int ch = lane % CPR;
+      uint4 v[CPR];
+#pragma unroll
+      for (int k = 0; k < CPR; ++k) {
+        const int rl = k * RPI + lane / CPR;
+        const long long o = __shfl_sync(0xffffffffu, off, rl);
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (32 * quarter + rl < u.nrows)
+          v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.q) + o + grp * (D / 2) + ch * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < CPR; ++k) *reinterpret_cast<uint4*>(at + (k * RPI + lane / CPR) * LD + ch * 16) = v[k];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < CPR; ++k) v[k] = *reinterpret_cast<const uint4*>(at + lane * LD + k * 16);
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 4) {
+        const uint32_t w[16] = {v[k].x ^ flip,     v[k].y ^ flip,     v[k].z ^ flip,     v[k].w ^ flip,
+                                v[k + 1].x ^ flip, v[k + 1].y ^ flip, v[k + 1].z ^ flip, v[k + 1].w ^ flip,
+                                v[k + 2].x ^ flip, v[k + 2].y ^ flip, v[k + 2].z ^ flip, v[k + 2].w ^ flip,
+                                v[k + 3].x ^ flip, v[k + 3].y ^ flip, v[k + 3].z ^ flip, v[k + 3].w ^ flip};
+        tmem_st_16(tmem + C::kQ + grp * (D / 4) + 4 * k + lanes, w);
+      }
+      tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::fence_proxy_async_smem();
+    } else {             // the warp's own 32 (with one row tile the groups take 16 each), 16 bytes a lane
       constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows of a warp's step
-      const long long off = b * c.qb + (long long)t_row * c.qt + (long long)h_row * c.qh;
-      const uint32_t flip = c.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale becomes -q and its magnitude
       uint8_t* qt = Qs + (two ? grp * C::QB : 0);
       const int r0 = two ? 0 : 16 * grp, nr = two ? 32 : 16, ch = lane % CPR;
       uint4 v[32 / RPI < 16 ? 32 / RPI : 16];     // all of a group's rows at once (32 at head_dim 256 are never asked of one)
@@ -450,24 +499,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4)) = v[k];
       }
       ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&q_ready[grp]);
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&q_ready[grp]);
     const float scale = fabsf(c.scale_log2);
     float m = -INFINITY, l = 0.f;                 // l counts in units of 2^m
-    int partial = 0;                              // steps with hidden keys so far
     // Whether key r of the tile of step q is seen; looked up a step ahead.
     auto sees = [&](int q) {
       if (q >= steps) return false;
-      const TileAt t = tile_at(u, u.t0 + (two ? q >> 1 : q));
+      const TileAt t = tile_at<KT>(u, u.t0 + (two ? q >> 1 : q));
       const uint8_t* mask = t.pre ? c.pre.mask : c.own.mask;
       return r < t.nk && (!mask || mask[(t.pre ? 0 : u.b * c.own.mask_sb) + t.k0 + r]);
     };
     bool next_vis = sees(grp);
     for (int q = grp; q < steps; q += 2) {
       const int j = two ? q >> 1 : q;
-      const TileAt t = tile_at(u, u.t0 + j);
-      const bool whole = !has_hidden(c, t);
+      const TileAt t = tile_at<KT>(u, u.t0 + j);
+      const bool whole = !has_hidden<KT>(c, t);
       if (!whole) {
         const uint32_t word = __ballot_sync(0xffffffffu, next_vis);
         // (the group's last look at the words of its previous step was before its P was complete)
@@ -478,14 +526,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       next_vis = sees(q + 2);
       wait(&s_full[grp], q >> 1);
       ptx::tc_fence_after();
-      const uint32_t s_tmem = tmem + grp * kTile + lanes;
+      const uint32_t s_tmem = tmem + grp * KT + lanes;
       if (live) {
-        uint32_t x[4][32];                        // the row of S
+        uint32_t x[KT / 32][32];                  // the row of S
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld_32_async(s_tmem + 32 * cc, x[cc]);
+        for (int cc = 0; cc < KT / 32; ++cc) tmem_ld_32_async(s_tmem + 32 * cc, x[cc]);
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < KT / 32; ++cc) {
           tmem_wait_ld(x[cc]);
           if (!whole) {
             const uint32_t vis = seen[grp * 4 + cc];
@@ -536,7 +584,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < KT / 32; ++cc) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -558,17 +606,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       if (!whole && !(two && grp)) {
         // hidden values become zeros: their weight is 0, and 0 times anything stored there must be 0
-        wait(&v_landed[grp], partial++);
-        const uint32_t hidden = ~seen[grp * 4 + quarter];
+        // (a stage's earlier uses had landed before S of this step, so its parity means this one)
+        const int cnt = order.of_v(j) * NC;
+        for (int cc = 0; cc < NC; ++cc) wait(&ready[(cnt + cc) % NST], (cnt + cc) / NST);
+        const uint32_t hidden = 32 * quarter < KT ? ~seen[grp * 4 + quarter] : 0u;
         if (hidden) {                             // (the same in the warp's lanes: 8 of them write a key's 128 bytes)
-          const int cnt = order.of_v(j) * NC;
 #pragma unroll 1
           for (int k = lane >> 3; k < 32; k += 4) {
             if (!((hidden >> k) & 1u)) continue;
             const int key = 32 * quarter + k;
             uint8_t* dst = ring + ((cnt + key / VK) % NST) * kStage + (key % VK) * 128 + (lane & 7) * 16;
 #pragma unroll
-            for (int dc = 0; dc < NC; ++dc) *reinterpret_cast<uint4*>(dst + dc * VK * 128) = make_uint4(0u, 0u, 0u, 0u);
+            for (int dc = 0; dc < C::DC; ++dc) *reinterpret_cast<uint4*>(dst + dc * VK * 128) = make_uint4(0u, 0u, 0u, 0u);
           }
           ptx::fence_proxy_async_smem();
         }
@@ -591,12 +640,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       l = l * (m == top ? 1.f : ex2(m - top)) + other.y * (other.x == top ? 1.f : ex2(other.x - top));
       m = top;
     }
-    const bool split = c.plan.n_slots > 1, first = two || grp == 0;
+    const bool join = c.plan.cluster > 1, split = c.plan.n_slots > 1 || join, first = two || grp == 0;
     const long long pr = part_row(c, u, row);
+    float2* ml_sm = reinterpret_cast<float2*>(Qs + C::kStaged);
     if (mine && first && split) {
       // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none
       const float mo = l != l ? INFINITY : l == 0.f ? -INFINITY : m;
-      *reinterpret_cast<float2*>(c.part_ml + pr * 2) = make_float2(mo, l);
+      *(join ? ml_sm + tile_row + r : reinterpret_cast<float2*>(c.part_ml + pr * 2)) = make_float2(mo, l);
     }
     if (mine && first && !split && c.lse)
       c.lse[((long long)b * c.Tq + t_row) * c.Hq + h_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -630,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
       }
       ptx::fence_proxy_async_smem();
-      if (mine) {
+      if (mine && !join) {
         if (split) {
           if (l != 0.f) bulk_store(c.part_o + pr * D + c0, stage, cols * 4);   // (the join does not read an empty part)
         } else if (c.out_tiled_rows == 0) {
@@ -643,6 +693,76 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if (join) {   // the ranges' parts of a row, in order: a warp takes four rows at a time, from every CTA of the cluster
+      __syncwarp();
+      ptx::cluster_sync();
+      constexpr int V = D >= 128 ? 4 : 2, NV = D / (32 * V), R = 4;   // elements of a lane's load, loads of a lane, rows
+      const int ranks = c.plan.cluster, rank = (int)ptx::cluster_ctarank();
+      const uint32_t ml_a = ptx::smem_u32(ml_sm), o_a = ptx::smem_u32(Qs) + lane * V * 4;
+      for (int p = (rank * 8 + warp - C::kSoft) * R; p < u.nrows; p += ranks * 8 * R) {
+        // lane 8 i + k: row p + i of CTA k
+        float2 part = make_float2(-INFINITY, 0.f);
+        if ((lane & 7) < ranks && p + (lane >> 3) < u.nrows)
+          part = ptx::ld_dsmem_f32x2(ptx::mapa(ml_a + (p + (lane >> 3)) * 8, lane & 7));
+        const unsigned jr = (unsigned)(u.row0 + p) + (lane >> 3), jb = jr / (unsigned)c.plan.rows_b, jx = jr - jb * (unsigned)c.plan.rows_b;
+        const unsigned jt = jx / (unsigned)c.group, jh = u.kvh * c.group + jx - jt * (unsigned)c.group;
+        float top = part.x;
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float w = part.x == -INFINITY ? 0.f : exp2f(part.x - top);
+        float sum = part.x == -INFINITY ? 0.f : w * part.y;
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        float acc[R][NV][V] = {};
+#pragma unroll 2
+        for (int k = 0; k < ranks; ++k) {
+          const uint32_t from = ptx::mapa(o_a + p * C::kRowBytes, k);   // (rows past the last lie behind it in the stage)
+          float v[R][NV][V];
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+              const uint32_t at = from + i * C::kRowBytes + j * 128 * V;
+              if (k == rank) {   // (its own memory is not read by way of the cluster, at a quarter of the rate)
+                const uint8_t* own = Qs + (p + i) * C::kRowBytes + j * 128 * V + lane * V * 4;
+                if (V == 4) *reinterpret_cast<float4*>(v[i][j]) = *reinterpret_cast<const float4*>(own);
+                else *reinterpret_cast<float2*>(v[i][j]) = *reinterpret_cast<const float2*>(own);
+              } else if (V == 4) *reinterpret_cast<float4*>(v[i][j]) = ptx::ld_dsmem_f32x4(at);
+              else *reinterpret_cast<float2*>(v[i][j]) = ptx::ld_dsmem_f32x2(at);
+            }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float wk = __shfl_sync(0xffffffffu, w, 8 * i + k);
+            const bool any = __shfl_sync(0xffffffffu, part.x, 8 * i + k) != -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+              for (int e = 0; e < V; ++e) acc[i][j][e] = any ? fmaf(wk, v[i][j][e], acc[i][j][e]) : acc[i][j][e];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float rtop = __shfl_sync(0xffffffffu, top, 8 * i), rsum = __shfl_sync(0xffffffffu, sum, 8 * i);
+          const unsigned rb = __shfl_sync(0xffffffffu, jb, 8 * i), rt = __shfl_sync(0xffffffffu, jt, 8 * i), rh = __shfl_sync(0xffffffffu, jh, 8 * i);
+          if (p + i >= u.nrows) break;
+          const float inv = rtop == -INFINITY ? 0.f : 1.f / rsum;
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            uint32_t* to = reinterpret_cast<uint32_t*>(out_bf16(c, rb, rt, rh, j * 32 * V + lane * V));
+            if (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(ptx::pack_bf16x2(acc[i][j][0] * inv, acc[i][j][1] * inv),
+                                                                   ptx::pack_bf16x2(acc[i][j][V - 2] * inv, acc[i][j][V - 1] * inv));
+            else *to = ptx::pack_bf16x2(acc[i][j][0] * inv, acc[i][j][1] * inv);
+          }
+          if (c.lse && lane == 0)
+            c.lse[((long long)rb * c.Tq + rt) * c.Hq + rh] = rtop == -INFINITY ? -INFINITY : (rtop + log2f(rsum)) * 0.6931471805599453f;
+        }
+      }
+    }
+  }
+  if (c.plan.cluster > 1) {
+    __syncwarp();
+    if (warp < C::kSoft) ptx::cluster_sync();     // (the softmax warps' before their join)
+    ptx::cluster_sync();                          // the others have read this CTA's rows
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -690,6 +810,14 @@ bool encode(CUtensorMap* m, const void* base, int D, int chunks, int keys, int l
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaLaunchAttribute cluster_of(int ranks) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ranks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  return at;
+}
+
 template <int D>
 cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
   using C = Cfg<D>;
@@ -700,8 +828,8 @@ cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
     *hm = c.Hkv > 1 && s.sh == 0 ? 0 : 1;
     *bm = batch > 1 && s.sb == 0 ? 0 : 1;
     const int heads = *hm ? c.Hkv : 1, nb = *bm ? batch : 1;
-    ok = ok && encode(k, s.k, D, 1, kTile, s.len, heads, s.st, s.sh, nb, s.sb) &&
-         encode(v, s.v, D, C::NC, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
+    ok = ok && encode(k, s.k, D, C::CK, C::KT, s.len, heads, s.st, s.sh, nb, s.sb) &&
+         encode(v, s.v, D, C::DC, C::VK, s.len, heads, s.st, s.sh, nb, s.sb);
   };
   int pre_b = 0;
   source(c.pre, 1, &m.pre_k, &m.pre_v, &m.pre_h, &pre_b);
@@ -709,16 +837,41 @@ cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   const long long elems = c.plan.decode ? 0 : (long long)c.B * c.plan.tiles_e * c.plan.ne;
   const dim3 grid((unsigned)((long long)c.plan.tiles_s * c.plan.ns + elems), c.Hkv);
-  attn_cache_kernel<D><<<grid, C::kThreads, C::kSmem, st>>>(c, m);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = cluster_of(c.plan.cluster);
+  cfg.attrs = &at;
+  cfg.numAttrs = c.plan.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_cache_kernel<D>, c, m);
 }
+
+// CTAs that run at once in clusters of 2 to 8 (the same on every GPU of this kind), by head_dim / 64 / 2.
+std::atomic<int> g_at_once[3][kMaxCluster + 1];
 
 template <int D>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_cache_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(attn_cache_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  for (int n = 2; n <= kMaxCluster && e == cudaSuccess; ++n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n * 256);
+    cfg.blockDim = dim3(Cfg<D>::kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cudaLaunchAttribute at = cluster_of(n);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, attn_cache_kernel<D>, &cfg);
+    g_at_once[D / 128][n] = clusters * n;
+  }
+  return e;
 }
 
 }  // namespace
+
+int attention_tc_at_once(int D, int ranks) { return g_at_once[D / 128][ranks]; }
 
 cudaError_t configure_attention_tc() {
   if (!encode_fn()) return cudaErrorNotSupported;

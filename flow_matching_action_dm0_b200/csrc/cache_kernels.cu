@@ -31,6 +31,10 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // codes = E4M3(x * 2^-e) (exact product, one rounding).  A row is D/8 lanes
 // of 8 elements; the maximum over the row's magnitudes is taken on their bit
 // patterns, which order like the values with infinities and NaN on top.
+// Bound by its bytes (bf16 read, codes written, a scale a row): four rows'
+// loads in flight a thread (one: 92 us), past L1 as nothing is read twice.
+// Measured on B200: 64 x 816 tokens x 8 heads x 128, 245 MB in 57 us, 4.3
+// TB/s (a copy reaches 6.6; some of the sequences are short).
 // ---------------------------------------------------------------------------
 constexpr int kRowsAhead = 4;                   // rows whose loads a thread has in flight
 
@@ -107,7 +111,9 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const __grid_constant__ C
   }
 }
 
-// Cache read: code * scale, rounded once.  A row is D/16 lanes of 16 codes.
+// Cache read: code * scale in fp32, rounded to T.  A row is D/16 lanes of 16
+// codes, 32 bytes of bf16 a lane.  Bound by its bytes as the write is: 72 x
+// 816 tokens x 4 heads, 333 MB in 65 us, 5.1 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ CacheCall c) {
   constexpr int LPR = D / 16;
@@ -172,7 +178,13 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Ca
 // columns 4 tx + 64 c of the output.  One pass over the keys with the running
 // maximum (base 2) and sum of each row.  The next keys are copied while the
 // values are used and the next values while the keys are.  Hidden keys score
-// -inf and are copied as zeros, whatever they hold.
+// -inf and are copied as zeros, whatever they hold.  The work is fp32 (no
+// tensor core keeps 24 bits), so the bound is the FMA pipe and, before it, the
+// shared memory that feeds it: 64 rows reuse a key or value four times from
+// registers, 16 rows (taken where a unit has no more) once.  Measured on
+// B200: 8 suffixes of 51 tokens x 4 heads of 64 dims over up to 561 keys, 21
+// us, 6 of them the join's; 3 suffixes of nine tokens over 73, 14 us, 11 of
+// them the kernel's.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
@@ -378,7 +390,8 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(const __grid_constant__ A
 // Join of a row's partial results: out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k.
 // `per` warps share a row, each taking every per-th slot with its loads in
 // flight together; their sums are added in warp order.  Empty parts (m = -inf)
-// do not count.
+// do not count.  Bound by the latency of its two dependent loads; it starts
+// while the attention ends and waits for it.
 template <typename QT, int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnCall c, int per) {
   constexpr int V = D >= 128 ? 4 : 2, NC = D / (32 * V);   // elements of a lane's load, loads of a lane
@@ -537,21 +550,33 @@ cudaError_t launch_kv_read(const CacheCall& c, cudaStream_t st) {
 
 // How many key ranges a unit's tiles are split over, and about how long the
 // launch then takes (us).  `fixed` is a CTA's start and end, `tile` a key tile
-// at an SM's full rate and `alone` with one CTA on it; a second range brings the join: its launch, and every row's parts written
-// and read.  (Measured on B200: 64 units of 128 rows x 7 tiles of head_dim 256
-// take 24.6 us in two ranges and their join, 18 us in one.)
+// at an SM's full rate and `alone` with one CTA on it; a second range brings
+// the join: its launch, and every row's parts written and read, or, for up to
+// eight ranges where `at_once` knows how many CTAs run in clusters of that
+// size, the cluster's own.  (Measured on B200, head_dim 256: 64 units of 128
+// rows x 816 keys take 22.4 us in one range, 20.5 in two that join in a
+// cluster and 26.5 in two with the join's launch; 32 units of 5070 keys 90 us
+// in one, 43 in a cluster of four, 49 in four with the join's launch.)
+constexpr float kClusterJoin = 2.f;   // us
 struct Split {
   int n;
+  bool cluster;
   float us;
 };
-static Split best_split(long long units, int tiles, int sms, int per_sm, float fixed, float tile, float alone, float join,
-                        float join_each) {
-  Split best{1, 1e30f};
+template <typename AtOnce>
+static Split best_split(long long units, int tiles, int slots, int per_sm, float fixed, float tile, float alone, float join,
+                        float join_each, AtOnce at_once) {
+  Split best{1, false, 1e30f};
   for (int n = 1; n <= std::min(std::max(tiles, 1), 64); ++n) {
-    const long long ctas = units * n, waves = (ctas + (long long)sms * per_sm - 1) / ((long long)sms * per_sm);
-    const float shared = (float)std::min<long long>(per_sm, (ctas + sms - 1) / sms) * tile;   // CTAs of an SM share its rate
-    const float us = (float)waves * (fixed + (float)((tiles + n - 1) / n) * std::max(alone, shared)) + (n > 1 ? join : 0.f) + join_each * n;
-    if (us < best.us) best = {n, us};
+    const long long ctas = units * n;
+    const float shared = (float)std::min<long long>(per_sm, (ctas + slots - 1) / slots) * tile;   // CTAs of an SM share its rate
+    const float range = fixed + (float)((tiles + n - 1) / n) * std::max(alone, shared);
+    auto waves = [&](long long together) { return (float)((ctas + together - 1) / together); };
+    const float us = waves((long long)slots * per_sm) * range + (n > 1 ? join : 0.f) + join_each * n;
+    if (us < best.us) best = {n, false, us};
+    const int together = n > 1 && n <= kMaxCluster ? at_once(n) : 0;
+    const float us_c = together ? waves(together) * (range + kClusterJoin) : 1e30f;
+    if (us_c < best.us) best = {n, true, us_c};
   }
   return best;
 }
@@ -574,7 +599,7 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
   const float join = 3.f, join_each = (float)(rows * c.Hkv * c.D) * 8.f / 4e6f;   // us: launch; a part of all rows at 4 TB/s
   auto tiles_of = [](long long keys, int kt) { return (int)((keys + kt - 1) / kt); };
   // Rows of a unit and its ranges, for `elems` elements of `rows_e` rows over `keys` keys.
-  auto shape = [&](long long elems, long long rows_e, long long keys, int kt, int* bm, int* tiles, int* n) {
+  auto shape = [&](long long elems, long long rows_e, long long keys, int kt, bool alone_kind, int* bm, int* tiles, int* n) {
     float best = 1e30f;
     const int choices[2] = {c.bf16 ? 128 : 16, c.bf16 ? attention_tc_rows(c.D) : 64};
     for (const int rows_u : choices) {
@@ -584,26 +609,29 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
       if (c.bf16) {
         // two row tiles share a CTA's loads
         fixed = 6.f;
-        tile = alone = c.D == 256 ? 1.5f : c.D == 128 ? (rows_u == 256 ? 1.95f : 1.1f) : (rows_u == 256 ? 1.5f : 0.9f);
+        tile = alone = c.D == 256 ? 0.85f : c.D == 128 ? (rows_u == 256 ? 1.95f : 1.1f) : (rows_u == 256 ? 1.5f : 0.9f);
       } else {
         fixed = 4.f;
         tile = (rows_u == 64 ? 2.6f : 1.f) * (float)c.D / 64.f;
         alone = (rows_u == 64 ? 4.5f : 3.f) * (float)c.D / 64.f;
         per_sm = std::max(1, 227 * 1024 / (attn_f32_smem(rows_u, c.D) + 1024));
       }
-      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), num_sms, per_sm, fixed, tile, alone, join, join_each);
+      // clusters: all of the call's units are of one kind and the tensor cores'
+      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), num_sms, per_sm, fixed, tile, alone, join, join_each,
+                                 [&](int ranks) { return c.bf16 && alone_kind ? attention_tc_at_once(c.D, ranks) : 0; });
       if (s.us < best) {
         best = s.us;
         *bm = rows_u;
         *tiles = (int)tu;
         *n = s.n;
+        p.cluster = s.cluster ? s.n : 1;
       }
     }
   };
-  p.kt_s = c.bf16 ? 128 : kKeys;
+  p.kt_s = c.bf16 ? attention_tc_keys(c.D) : kKeys;
   p.kt_e = p.decode ? 16 * decode_groups(c.D) : p.kt_s;
   p.bm_s = c.bf16 ? 128 : 64;
-  if (stack) shape(1, rows, c.pre.len, p.kt_s, &p.bm_s, &p.tiles_s, &p.ns);
+  if (stack) shape(1, rows, c.pre.len, p.kt_s, c.own.len == 0, &p.bm_s, &p.tiles_s, &p.ns);
   if (!stack || c.own.len > 0) {
     const long long keys = (long long)c.own.len + (p.prefix_in_elem ? c.pre.len : 0);
     if (p.decode) {
@@ -617,7 +645,7 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
         if (p.ne <= 8) p.cluster = p.ne;
       }
     } else {
-      shape(c.B, p.rows_b, keys, p.kt_e, &p.bm_e, &p.tiles_e, &p.ne);
+      shape(c.B, p.rows_b, keys, p.kt_e, !stack, &p.bm_e, &p.tiles_e, &p.ne);
     }
   }
   p.n_slots = p.cluster > 1 ? 1 : p.ns + p.ne;

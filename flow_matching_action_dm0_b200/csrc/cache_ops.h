@@ -29,8 +29,8 @@ struct KvSource {
 // the whole batch over a range of the prefix; element units take bm_e rows of
 // one element over a range of [prefix ; own keys] (prefix_in_elem) or of its
 // own keys.  Each row has n_slots partial results (slot = range), joined by
-// combine_kernel when there is more than one; the ranges of a decode unit
-// that form a cluster join in it and count as one.
+// combine_kernel when there is more than one; ranges of a unit that form a
+// cluster join in it and count as one.
 struct AttnPlan {
   int bm_s, bm_e;              // rows of a stacked and of an element unit
   int kt_s, kt_e;              // keys of their tiles
@@ -39,7 +39,7 @@ struct AttnPlan {
   int tiles_e, ne;             // element units: row tiles per element, key ranges (0: none)
   int prefix_in_elem;          // element units read the prefix too
   int decode;                  // element units are the few-row kernel's
-  int cluster;                 // its CTAs that join by distributed shared memory (1: none)
+  int cluster;                 // a unit's ranges, whose CTAs join by distributed shared memory (1: not so)
   int unpack_pre, unpack_own;  // E4M3 sources that are read back to bf16 in the workspace first
   int n_slots;                 // partial results of a row
 };
@@ -78,10 +78,13 @@ cudaError_t configure_attention();
 cudaError_t configure_attention_tc();
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st);
 int attention_tc_rows(int D);   // rows of a CTA
+constexpr int attention_tc_keys(int D) { return D == 256 ? 64 : 128; }   // keys of a tile
+int attention_tc_at_once(int D, int ranks);   // CTAs that run at once in clusters of `ranks` (0: unknown)
 // The few-row kernel (bf16 queries, 16 rows of an element or less).
 cudaError_t configure_attention_decode();
 cudaError_t launch_attention_decode(const AttnCall& c, cudaStream_t st);
 constexpr int kDecodeRows = 16;
+constexpr int kMaxCluster = 8;
 constexpr int decode_groups(int D) { return D == 256 ? 6 : 4; }                          // of 16 keys each, in a tile
 constexpr int attention_decode_ctas(int D) { return D == 256 ? 1 : D == 128 ? 3 : 4; }   // CTAs of an SM
 
@@ -138,8 +141,10 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
   int split, nsplit, kt;
   if (x < stacked) {
     kt = p.kt_s;
-    split = (int)(x / (unsigned)p.tiles_s);
-    const int tile = (int)(x - (unsigned)split * p.tiles_s);
+    const bool by_range = p.cluster > 1;   // a cluster's CTAs are neighbours; otherwise those of a range are
+    const unsigned inner = by_range ? p.ns : p.tiles_s, y = x / inner, z = x - y * inner;
+    split = (int)(by_range ? z : y);
+    const int tile = (int)(by_range ? y : z);
     nsplit = p.ns;
     u.slot = split;
     u.b = 0;
@@ -150,10 +155,13 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnCall& c) {
   } else {
     x -= stacked;
     kt = p.kt_e;
-    const unsigned y = x / (unsigned)p.tiles_e;
-    const int tile = (int)(x - y * p.tiles_e);
-    u.b = (int)(y / (unsigned)p.ne);
-    split = (int)(y - (unsigned)u.b * p.ne);
+    const bool by_range = p.cluster > 1;
+    const unsigned inner = by_range ? p.ne : p.tiles_e, outer = by_range ? p.tiles_e : p.ne;
+    const unsigned y = x / inner, z = x - y * inner;
+    u.b = (int)(y / outer);
+    const unsigned w = y - (unsigned)u.b * outer;
+    split = (int)(by_range ? z : w);
+    const int tile = (int)(by_range ? w : z);
     nsplit = p.ne;
     u.slot = p.n_slots > 1 ? p.ns + split : 0;
     u.row0 = (long long)u.b * p.rows_b + (long long)tile * p.bm_e;
