@@ -34,7 +34,7 @@
 // share of the rows; more are joined by combine_kernel.
 //
 // What it reaches, and what bounds it (B200, cold L2): 2050 queries x 4001
-// keys x 4 elements at head_dim 128, 305-310 us, 870 TFLOP/s of the 1657 a
+// keys x 4 elements at head_dim 128, 305-312 us, 870 TFLOP/s of the 1657 a
 // matrix product reaches: a step's chain S -> softmax -> P V, of which the
 // exponentials and their conversion are the longest part, fills the time of
 // two steps' products, and 528 CTAs on 148 SMs leave the last of four waves

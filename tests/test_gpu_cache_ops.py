@@ -601,3 +601,25 @@ def test_places_and_sizes_that_do_not_fit_are_refused(ops):
         with pytest.raises(ValueError):
             call()
     assert (cache.k_scale == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tk", [130, 260, 520, 1000, 1500, 4000])
+def test_key_ranges_join(ops, d, tk):
+    """Few units over many keys: two to eight ranges of a unit that join in a cluster, and more by a second launch;
+    an element's lengths leave some of them empty, or all."""
+    cross_case(ops, "bf16", "bf16", 3, 40, tk, 8, 1, d, lens=[tk, 70, 0], masked=True)
+    cross_case(ops, "bf16", "bf16", 1, 17, tk, 1, 1, d)
+    cross_case(ops, "bf16", "fp8", 2, 3, tk, 8, 1, d, lens=[1, tk])
+    shared_case(ops, "bf16", "bf16", 3, 20, tk, None, 8, 1, d, masked=tk == 1000)
+    shared_case(ops, "bf16", "bf16", 2, 40, tk, 130, 8, 1, d, lens=[0, 130], masked=True)
+
+
+def test_a_nan_in_one_key_range_reaches_its_rows_alone(ops):
+    g = gen(34)
+    q, k, v = rand(g, 2, 40, 8, 256), rand(g, 2, 1000, 1, 256), rand(g, 2, 1000, 1, 256)
+    q[0, 5, 3] = float("nan")
+    k[1, 900] = float("inf")
+    out, lse = ops.cross_attention(q, (k, v), lens=ints([1000, 900]), lse=True)
+    bad = torch.isnan(out).any(-1)
+    assert bad[0, 5, 3] and bad.sum() == 1 and torch.isnan(lse[0, 5, 3]) and torch.isfinite(lse).sum() == lse.numel() - 1
