@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
         c.lse[((long long)u.b * c.Tq + t) * c.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
+  if (c.plan.ns) ptx::pdl_wait();                   // the prefix's grid: combine_kernel waits for this one alone
   if (ranks == 1) return;
   // The CTAs of the cluster, in order, by distributed shared memory.
   ptx::cluster_sync();
@@ -492,13 +493,17 @@ cudaError_t launch(const AttnCall& c, cudaStream_t st) {
   cfg.blockDim = dim3(Cfg<D, F8>::kThreads);
   cfg.dynamicSmemBytes = Cfg<D, F8>::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = c.plan.cluster;
-  at.val.clusterDim.y = 1;
-  at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c.plan.cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // Beside the prefix's grid, which it does not need: that one's CTAs are all
+  // running, and all that came before it has ended, when this one may start.
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = c.plan.ns ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, F8>, c, c.plan.cluster);
 }
 
