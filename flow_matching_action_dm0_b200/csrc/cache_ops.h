@@ -70,7 +70,7 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms);
 size_t attention_workspace(const AttnCall& c);
 // Enqueues a planned call; workspace as above.
 cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st);
-// Plans and enqueues a call whose workspace is given; splits no keys where it is too small.
+// Plans and enqueues a call whose workspace is given; makes fewer ranges of the keys where it is too small.
 cudaError_t run_attention(AttnCall& c, int num_sms, void* workspace, size_t workspace_bytes, cudaStream_t st);
 // Sets the kernels' attributes on the current device (outside any capture).
 cudaError_t configure_attention();
