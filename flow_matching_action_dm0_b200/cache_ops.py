@@ -26,6 +26,7 @@ import torch
 
 from . import _lib as L
 from ._lib import RTV_BF16, RTV_F32, RTV_FP8_E4M3, rtv_kv, rtv_queries
+from .expert import on_stream
 
 _CODES = {torch.float32: RTV_F32, torch.bfloat16: RTV_BF16}
 _TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -79,14 +80,7 @@ class CacheOps:
 
     # ------------------------------------------------------------------
     def _on(self, stream):
-        """Context in which torch allocates for, and names, the call's stream."""
-        if isinstance(stream, torch.cuda.Stream):
-            if stream.device_index != self.device:
-                raise ValueError(f"stream: of cuda:{stream.device_index}, not the handle's GPU (cuda:{self.device})")
-        else:
-            stream = torch.cuda.ExternalStream(int(stream), device=self._torch_device) if stream else \
-                torch.cuda.default_stream(self._torch_device)
-        return torch.cuda.stream(stream)
+        return on_stream(stream, self.device)
 
     def _stream(self) -> int:
         return torch._C._cuda_getCurrentRawStream(self.device)   # torch.cuda.current_stream without its object

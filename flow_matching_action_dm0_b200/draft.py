@@ -18,7 +18,7 @@ from typing import Dict, NamedTuple, Optional, Sequence
 import numpy as np
 
 from . import _lib as L
-from .expert import _DTYPES, ActionExpert, _ptr, _stream, make_tensors, to_dtype_bits
+from .expert import _DTYPES, ActionExpert, _ptr, _result, _stream, make_tensors, to_dtype_bits
 
 
 def make_draft_config(shape, max_vis: Optional[int] = None, max_batch: Optional[int] = None) -> L.rtv_draft_config:
@@ -57,16 +57,11 @@ class DraftModel:
             vis = np.ascontiguousarray(vis)
         b, v = int(vis.shape[0]), int(vis.shape[1])
         if out is None:
-            if isinstance(vis, np.ndarray):
-                out = np.empty((b, self.cfg.n_queries, self.cfg.action_dim), dtype=np.float32)
-            else:
-                import torch
-                out = torch.empty((b, self.cfg.n_queries, self.cfg.action_dim), dtype=torch.float32,
-                                  device=vis.device)
+            out = _result(vis, (b, self.cfg.n_queries, self.cfg.action_dim), stream, self.device)
         pv, _ = _ptr(vis)
         po, _ = _ptr(out)
         self._keep = [vis]
-        L.rtv_draft_forward(self.h, pv, v, b, po, _stream(stream))
+        L.rtv_draft_forward(self.h, pv, v, b, po, _stream(stream, self.device))
         if isinstance(out, np.ndarray):
             self.synchronize()
         return out
@@ -117,11 +112,7 @@ def flash_round(expert: ActionExpert, draft: DraftModel, vis, noise, state, taus
         vis = np.ascontiguousarray(vis)
     taus_h = np.ascontiguousarray(np.asarray(taus, dtype=np.float32))
     if out is None:
-        shape = (expert.cfg.chunk_len, expert.cfg.action_dim)
-        if isinstance(noise, np.ndarray):
-            out = np.empty(shape, dtype=np.float32)
-        else:
-            out = noise.new_empty(shape)
+        out = _result(noise, (expert.cfg.chunk_len, expert.cfg.action_dim), stream, expert.device)
     acc = np.zeros(1, dtype=np.int32)
     flags = np.zeros(1, dtype=np.uint32)
     full = np.zeros(1, dtype=np.int32)
@@ -131,5 +122,5 @@ def flash_round(expert: ActionExpert, draft: DraftModel, vis, noise, state, taus
     po, _ = _ptr(out)
     L.rtv_flash_round(expert.h, draft.h, pv, int(vis.shape[0]), pn, ps, taus_h.ctypes.data, len(taus_h), float(delta),
                       int(gripper_dim), int(n_steps), po, acc.ctypes.data, flags.ctypes.data, full.ctypes.data,
-                      _stream(stream))
+                      _stream(stream, expert.device))
     return RoundResult(out, int(acc[0]), int(flags[0]), bool(full[0]))

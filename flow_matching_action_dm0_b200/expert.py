@@ -12,10 +12,14 @@
 ``shape`` is any object with the rtv_expert_config field names (n_layers,
 width, n_q_heads, ...; dtype "f32"/"bf16").  Arrays may be numpy (host) or
 torch tensors (host or CUDA); pointers are handed to the C ABI unchanged.
+``stream`` is a torch stream or its address; None is torch's current stream of
+the context's GPU.  Results are allocated for the stream that the work goes
+to, as if the call were made inside ``torch.cuda.stream(stream)``.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from typing import Dict, Optional, Sequence, Tuple
 
@@ -61,14 +65,52 @@ def _ptr(a) -> Tuple[int, bool]:
     raise TypeError(f"unsupported array type {type(a)}")
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: Optional[int] = None) -> int:
     if stream is None:
         try:
             import torch
-            return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+            return torch.cuda.current_stream(device).cuda_stream if torch.cuda.is_available() else 0
         except Exception:  # pragma: no cover
             return 0
     return int(getattr(stream, "cuda_stream", stream))
+
+
+def on_stream(stream, device: int):
+    """Context in which torch allocates on GPU ``device`` for the call's
+    stream (None: its current one), and names it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    dev = torch.device("cuda", device)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:
+            raise ValueError(f"stream: of cuda:{stream.device_index}, not the handle's GPU (cuda:{device})")
+    else:
+        address = _stream(stream)
+        stream = torch.cuda.ExternalStream(address, device=dev) if address else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def _result(a, shape, stream, device: int):
+    """An fp32 array of ``shape`` beside a: numpy, or torch on a's device, on
+    the handle's GPU taken from the pool of the stream that writes it."""
+    if isinstance(a, np.ndarray):
+        return np.empty(shape, dtype=np.float32)
+    import torch
+    with on_stream(stream if a.is_cuda and a.get_device() == device else None, device):
+        return a.new_empty(shape, dtype=torch.float32)
+
+
+def _used_on(stream, device: int, *tensors):
+    """The stream's queued work uses the tensors: their memory is not handed
+    out again before it is done, should they be released."""
+    mine = [t for t in tensors if not isinstance(t, np.ndarray) and t.is_cuda and t.get_device() == device]
+    if not mine:
+        return
+    import torch
+    with on_stream(stream, device):
+        for t in mine:
+            t.record_stream(torch.cuda.current_stream(device))
 
 
 def _dtype_code(name: str, a, matrix_dtype: int, overrides) -> int:
@@ -146,19 +188,16 @@ class ActionExpert:
         p = int(prefix_len if prefix_len is not None else kv.shape[3])
         ptr, _ = _ptr(kv)
         self._keep = [kv]
-        L.rtv_set_prefix_kv(self.h, ptr, p, b, _stream(stream))
+        L.rtv_set_prefix_kv(self.h, ptr, p, b, _stream(stream, self.device))
 
     def denoise(self, noise, state, n_steps: int, out=None, stream=None):
         """Action chunk [B][H][A] fp32.  noise/state/out: numpy or torch fp32."""
         if out is None:
-            if isinstance(noise, np.ndarray):
-                out = np.empty_like(noise, dtype=np.float32)
-            else:
-                out = noise.new_empty(noise.shape)
+            out = _result(noise, noise.shape, stream, self.device)
         pn, _ = _ptr(noise)
         ps, _ = _ptr(state)
         po, _ = _ptr(out)
-        L.rtv_denoise(self.h, pn, ps, int(n_steps), po, _stream(stream))
+        L.rtv_denoise(self.h, pn, ps, int(n_steps), po, _stream(stream, self.device))
         if isinstance(out, np.ndarray):
             self.synchronize(stream)
         return out
@@ -172,14 +211,12 @@ class ActionExpert:
         if out is not None and tuple(out.shape) != tuple(noise.shape):
             raise ValueError("out: the noise's shape expected")
         if out is None:
-            if isinstance(noise, np.ndarray):
-                out = np.empty_like(noise, dtype=np.float32)
-            else:
-                out = noise.new_empty(noise.shape)
+            out = _result(noise, noise.shape, stream, self.device)
         pn, _ = _ptr(noise)
         ps, _ = _ptr(state)
         po, _ = _ptr(out)
-        L.rtv_denoise_shared(self.h, pn, ps, int(noise.shape[0]), int(n_steps), po, _stream(stream))
+        L.rtv_denoise_shared(self.h, pn, ps, int(noise.shape[0]), int(n_steps), po, _stream(stream, self.device))
+        _used_on(stream, self.device, noise, state, out)
         if isinstance(out, np.ndarray):
             self.synchronize(stream)
         return out
@@ -191,16 +228,16 @@ class ActionExpert:
         import torch
         dev = torch.device("cuda", self.device)
         shape = (self.cfg.n_layers, 2, int(batch), self.cfg.n_kv_heads, int(prefix_len))
-        codes = torch.empty(shape + (self.cfg.head_dim,), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty(shape, dtype=torch.float32, device=dev)
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
+        with on_stream(stream, self.device):   # (the memory is the stream's: no other one's queued work still uses it)
+            codes = torch.empty(shape + (self.cfg.head_dim,), dtype=torch.float8_e4m3fn, device=dev)
+            scales = torch.empty(shape, dtype=torch.float32, device=dev)
         L.rtv_get_prefix_kv_quantized(self.h, codes.data_ptr(), scales.data_ptr(), int(prefix_len), int(batch),
-                                      _stream(stream))
+                                      _stream(stream, self.device))
         return codes, scales
 
     def set_prefix_kv_quantized(self, codes, scales, stream=None):
-        """Install what get_prefix_kv_quantized gave."""
+        """Install what get_prefix_kv_quantized gave (it may be released at
+        once: its memory is kept until the stream has read it)."""
         if codes.shape[:-1] != scales.shape or tuple(codes.shape[:2]) != (self.cfg.n_layers, 2) or \
                 tuple(codes.shape[3::2]) != (self.cfg.n_kv_heads, self.cfg.head_dim):
             raise ValueError("codes [L][2][B][Hkv][P][D] and scales [L][2][B][Hkv][P] expected")
@@ -208,8 +245,9 @@ class ActionExpert:
             raise TypeError("E4M3 codes and fp32 scales expected")
         pc, _ = _ptr(codes)
         ps, _ = _ptr(scales)
-        self._keep = [codes, scales]
-        L.rtv_set_prefix_kv_quantized(self.h, pc, ps, int(codes.shape[4]), int(codes.shape[2]), _stream(stream))
+        L.rtv_set_prefix_kv_quantized(self.h, pc, ps, int(codes.shape[4]), int(codes.shape[2]),
+                                      _stream(stream, self.device))
+        _used_on(stream, self.device, codes, scales)
 
     def verify(self, draft, noise, state, taus: Sequence[float], delta: float, gripper_dim: int,
                want_dist: bool = True, stream=None):
@@ -225,7 +263,7 @@ class ActionExpert:
         ps, _ = _ptr(state)
         L.rtv_verify(self.h, pd, pe, ps, taus_h.ctypes.data, len(taus_h), float(delta), int(gripper_dim),
                      acc.ctypes.data, flags.ctypes.data, dist.ctypes.data if dist is not None else 0,
-                     _stream(stream))
+                     _stream(stream, self.device))
         self.synchronize(stream)
         return int(acc[0]), int(flags[0]), dist
 

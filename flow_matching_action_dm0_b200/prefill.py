@@ -18,7 +18,7 @@ from typing import Dict, Optional
 import numpy as np
 
 from . import _lib as L
-from .expert import _DTYPES, ActionExpert, _ptr, _stream, make_tensors, to_dtype_bits
+from .expert import _DTYPES, ActionExpert, _ptr, _result, _stream, make_tensors, to_dtype_bits
 
 
 def make_prefill_config(shape, max_tokens: Optional[int] = None) -> L.rtv_prefill_config:
@@ -58,7 +58,7 @@ class PrefillStack:
         """Install the cache of emb [P][w] as the expert's prefix (batch 1)."""
         emb = self._emb(emb)
         pe, _ = _ptr(emb)
-        L.rtv_prefill_kv(self.h, expert.h, pe, int(emb.shape[0]), _stream(stream))
+        L.rtv_prefill_kv(self.h, expert.h, pe, int(emb.shape[0]), _stream(stream, self.device))
         if isinstance(emb, np.ndarray):
             expert.synchronize()
 
@@ -67,15 +67,13 @@ class PrefillStack:
         noise [H][A], state [Sd]."""
         emb = self._emb(emb)
         if out is None:
-            if isinstance(noise, np.ndarray):
-                out = np.empty_like(noise, dtype=np.float32)
-            else:
-                out = noise.new_empty(noise.shape)
+            out = _result(noise, noise.shape, stream, self.device)
         pe, _ = _ptr(emb)
         pn, _ = _ptr(noise)
         ps, _ = _ptr(state)
         po, _ = _ptr(out)
-        L.rtv_prefill_denoise(self.h, expert.h, pe, int(emb.shape[0]), pn, ps, int(n_steps), po, _stream(stream))
+        L.rtv_prefill_denoise(self.h, expert.h, pe, int(emb.shape[0]), pn, ps, int(n_steps), po,
+                              _stream(stream, self.device))
         if isinstance(out, np.ndarray):
             expert.synchronize()
         return out

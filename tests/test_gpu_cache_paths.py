@@ -186,3 +186,45 @@ def test_denoise_shared_shapes(cuda_ok):
     with pytest.raises(ValueError):
         ex.denoise_shared(noise, state, 2, out=np.zeros_like(noise[:1]))
     ex.close()
+
+
+def test_park_and_install_on_a_stream_of_their_own(cuda_ok):
+    """Nothing is synchronised: memory that another stream's queued work still
+    writes is not the parked prefix's, and arrays that are released at once
+    are read before their memory serves again."""
+    cfg = get_config("pi0-bf16", n_layers=2, prefix_len=100)
+    ex, W, kv = expert(cfg, 1)
+    noise = torch.from_numpy(np.ascontiguousarray(make_noise(cfg))).cuda()
+    state = torch.from_numpy(np.ascontiguousarray(make_state(cfg))).cuda()
+    ex.set_prefix_kv_quantized(*ex.get_prefix_kv_quantized(cfg.prefix_len))
+    # (a row whose largest value was rounded down to 224 * scale takes half the scale now)
+    codes, scales = ex.get_prefix_kv_quantized(cfg.prefix_len)
+    want = ex.denoise(noise, state, 2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)                     # the current stream is some 10 ms behind
+        junk = torch.empty_like(codes.view(torch.uint8))
+        junk.fill_(0x55)
+        del junk
+        mine = ex.get_prefix_kv_quantized(cfg.prefix_len, stream=stream)
+        with torch.cuda.stream(side):
+            kept = [t.view(torch.uint8).clone() for t in mine]
+        torch.cuda.synchronize()
+        same = [bool(torch.equal(x, y.view(torch.uint8))) for x, y in zip(kept, (codes, scales))]
+        assert same == [True, True]
+        given = codes.clone(), scales.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        ex.set_prefix_kv_quantized(*given, stream=stream)
+        del given
+        for t in (codes, scales):
+            torch.empty_like(t.view(torch.uint8)).fill_(0x11)
+        got = ex.denoise(noise, state, 2, stream=stream)
+        shared = ex.denoise_shared(noise, state[0], 2, stream=stream)
+        torch.cuda.synchronize()
+        assert bool(torch.equal(got, want))
+        assert bf16_tolerance_ok(shared.cpu().numpy(), want.cpu().numpy(), rel=2e-2, abs_=6e-2)
+    assert ex.status() == (0, 0)
+    ex.close()
