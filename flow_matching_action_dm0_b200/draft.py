@@ -18,7 +18,7 @@ from typing import Dict, NamedTuple, Optional, Sequence
 import numpy as np
 
 from . import _lib as L
-from .expert import _DTYPES, ActionExpert, _ptr, _result, _stream, make_tensors, to_dtype_bits
+from .expert import _DTYPES, ActionExpert, _f32, _ptr, _result, _stream, make_tensors, to_dtype_bits
 
 
 def make_draft_config(shape, max_vis: Optional[int] = None, max_batch: Optional[int] = None) -> L.rtv_draft_config:
@@ -59,7 +59,7 @@ class DraftModel:
         if out is None:
             out = _result(vis, (b, self.cfg.n_queries, self.cfg.action_dim), stream, self.device)
         pv, _ = _ptr(vis)
-        po, _ = _ptr(out)
+        po = _f32(out, "out")
         self._keep = [vis]
         L.rtv_draft_forward(self.h, pv, v, b, po, _stream(stream, self.device))
         if isinstance(out, np.ndarray):
@@ -117,9 +117,7 @@ def flash_round(expert: ActionExpert, draft: DraftModel, vis, noise, state, taus
     flags = np.zeros(1, dtype=np.uint32)
     full = np.zeros(1, dtype=np.int32)
     pv, _ = _ptr(vis)
-    pn, _ = _ptr(noise)
-    ps, _ = _ptr(state)
-    po, _ = _ptr(out)
+    pn, ps, po = _f32(noise, "noise"), _f32(state, "state"), _f32(out, "out")
     L.rtv_flash_round(expert.h, draft.h, pv, int(vis.shape[0]), pn, ps, taus_h.ctypes.data, len(taus_h), float(delta),
                       int(gripper_dim), int(n_steps), po, acc.ctypes.data, flags.ctypes.data, full.ctypes.data,
                       _stream(stream, expert.device))

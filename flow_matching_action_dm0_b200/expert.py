@@ -65,6 +65,14 @@ def _ptr(a) -> Tuple[int, bool]:
     raise TypeError(f"unsupported array type {type(a)}")
 
 
+def _f32(a, what: str) -> int:
+    """Address of a contiguous fp32 array (the library reads and writes four bytes an element)."""
+    ptr, _ = _ptr(a)
+    if str(a.dtype) not in ("float32", "torch.float32"):
+        raise TypeError(f"{what}: dtype {a.dtype}, fp32 expected")
+    return ptr
+
+
 def _stream(stream, device: Optional[int] = None) -> int:
     if stream is None:
         try:
@@ -194,9 +202,7 @@ class ActionExpert:
         """Action chunk [B][H][A] fp32.  noise/state/out: numpy or torch fp32."""
         if out is None:
             out = _result(noise, noise.shape, stream, self.device)
-        pn, _ = _ptr(noise)
-        ps, _ = _ptr(state)
-        po, _ = _ptr(out)
+        pn, ps, po = _f32(noise, "noise"), _f32(state, "state"), _f32(out, "out")
         L.rtv_denoise(self.h, pn, ps, int(n_steps), po, _stream(stream, self.device))
         if isinstance(out, np.ndarray):
             self.synchronize(stream)
@@ -212,9 +218,7 @@ class ActionExpert:
             raise ValueError("out: the noise's shape expected")
         if out is None:
             out = _result(noise, noise.shape, stream, self.device)
-        pn, _ = _ptr(noise)
-        ps, _ = _ptr(state)
-        po, _ = _ptr(out)
+        pn, ps, po = _f32(noise, "noise"), _f32(state, "state"), _f32(out, "out")
         L.rtv_denoise_shared(self.h, pn, ps, int(noise.shape[0]), int(n_steps), po, _stream(stream, self.device))
         _used_on(stream, self.device, noise, state, out)
         if isinstance(out, np.ndarray):
@@ -258,9 +262,7 @@ class ActionExpert:
         flags = np.zeros(1, dtype=np.uint32)
         h_len = self.cfg.chunk_len
         dist = np.zeros((len(taus_h), h_len), dtype=np.float32) if want_dist else None
-        pd, _ = _ptr(draft)
-        pe, _ = _ptr(noise)
-        ps, _ = _ptr(state)
+        pd, pe, ps = _f32(draft, "draft"), _f32(noise, "noise"), _f32(state, "state")
         L.rtv_verify(self.h, pd, pe, ps, taus_h.ctypes.data, len(taus_h), float(delta), int(gripper_dim),
                      acc.ctypes.data, flags.ctypes.data, dist.ctypes.data if dist is not None else 0,
                      _stream(stream, self.device))

@@ -18,7 +18,7 @@ from typing import Dict, Optional
 import numpy as np
 
 from . import _lib as L
-from .expert import _DTYPES, ActionExpert, _ptr, _result, _stream, make_tensors, to_dtype_bits
+from .expert import _DTYPES, ActionExpert, _f32, _ptr, _result, _stream, make_tensors, to_dtype_bits
 
 
 def make_prefill_config(shape, max_tokens: Optional[int] = None) -> L.rtv_prefill_config:
@@ -69,9 +69,7 @@ class PrefillStack:
         if out is None:
             out = _result(noise, noise.shape, stream, self.device)
         pe, _ = _ptr(emb)
-        pn, _ = _ptr(noise)
-        ps, _ = _ptr(state)
-        po, _ = _ptr(out)
+        pn, ps, po = _f32(noise, "noise"), _f32(state, "state"), _f32(out, "out")
         L.rtv_prefill_denoise(self.h, expert.h, pe, int(emb.shape[0]), pn, ps, int(n_steps), po,
                               _stream(stream, self.device))
         if isinstance(out, np.ndarray):
