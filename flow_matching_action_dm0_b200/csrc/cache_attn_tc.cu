@@ -43,7 +43,6 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "cache_ops.h"
 #include "common.cuh"
@@ -848,11 +847,8 @@ cudaError_t launch_tc(const AttnCall& c, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, attn_cache_kernel<D>, c, m);
 }
 
-// CTAs that run at once in clusters of 2 to 8 (the same on every GPU of this kind), by head_dim / 64 / 2.
-std::atomic<int> g_at_once[3][kMaxCluster + 1];
-
 template <int D>
-cudaError_t configure() {
+cudaError_t configure(AttnDevice* dev) {
   cudaError_t e = cudaFuncSetAttribute(attn_cache_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   for (int n = 2; n <= kMaxCluster && e == cudaSuccess; ++n) {
     cudaLaunchConfig_t cfg = {};
@@ -864,20 +860,18 @@ cudaError_t configure() {
     cfg.numAttrs = 1;
     int clusters = 0;
     e = cudaOccupancyMaxActiveClusters(&clusters, attn_cache_kernel<D>, &cfg);
-    g_at_once[D / 128][n] = clusters * n;
+    dev->at_once[D / 128][n] = clusters * n;
   }
   return e;
 }
 
 }  // namespace
 
-int attention_tc_at_once(int D, int ranks) { return g_at_once[D / 128][ranks]; }
-
-cudaError_t configure_attention_tc() {
+cudaError_t configure_attention_tc(AttnDevice* dev) {
   if (!encode_fn()) return cudaErrorNotSupported;
-  cudaError_t e = configure<64>();
-  if (e == cudaSuccess) e = configure<128>();
-  if (e == cudaSuccess) e = configure<256>();
+  cudaError_t e = configure<64>(dev);
+  if (e == cudaSuccess) e = configure<128>(dev);
+  if (e == cudaSuccess) e = configure<256>(dev);
   return e;
 }
 

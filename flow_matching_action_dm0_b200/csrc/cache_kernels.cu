@@ -581,7 +581,7 @@ static Split best_split(long long units, int tiles, int slots, int per_sm, float
   return best;
 }
 
-AttnPlan plan_attention(const AttnCall& c, int num_sms) {
+AttnPlan plan_attention(const AttnCall& c, const AttnDevice& dev) {
   AttnPlan p{};
   p.rows_b = c.Tq * c.group;
   p.cluster = 1;
@@ -617,8 +617,8 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
         per_sm = std::max(1, 227 * 1024 / (attn_f32_smem(rows_u, c.D) + 1024));
       }
       // clusters: all of the call's units are of one kind and the tensor cores'
-      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), num_sms, per_sm, fixed, tile, alone, join, join_each,
-                                 [&](int ranks) { return c.bf16 && alone_kind ? attention_tc_at_once(c.D, ranks) : 0; });
+      const Split s = best_split(elems * tu * c.Hkv, tiles_of(keys, kt), dev.num_sms, per_sm, fixed, tile, alone, join, join_each,
+                                 [&](int ranks) { return c.bf16 && alone_kind ? dev.at_once[c.D / 128][ranks] : 0; });
       if (s.us < best) {
         best = s.us;
         *bm = rows_u;
@@ -637,7 +637,7 @@ AttnPlan plan_attention(const AttnCall& c, int num_sms) {
     if (p.decode) {
       p.bm_e = kDecodeRows;
       p.tiles_e = 1;
-      const long long units = (long long)c.B * c.Hkv, slots = (long long)attention_decode_ctas(c.D) * num_sms;
+      const long long units = (long long)c.B * c.Hkv, slots = (long long)attention_decode_ctas(c.D) * dev.num_sms;
       p.ne = (int)std::max(1LL, std::min<long long>({slots / units, tiles_of(keys, p.kt_e), 64}));
       // Up to eight ranges join in a cluster, without a second launch.
       if (!stack && p.ne > 1) {
@@ -699,16 +699,19 @@ size_t attention_workspace(const AttnCall& c) {
          (c.plan.unpack_own ? 2 * unpacked_bytes(c, c.own, c.B) : 0);
 }
 
-cudaError_t configure_attention() {
-  cudaError_t e = cudaSuccess;
+cudaError_t configure_attention(AttnDevice* dev) {
+  *dev = AttnDevice{};
+  int id = 0;
+  cudaError_t e = cudaGetDevice(&id);
   auto chain = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
+  chain(cudaDeviceGetAttribute(&dev->num_sms, cudaDevAttrMultiProcessorCount, id));
   chain(set_smem<64, 16>());
   chain(set_smem<64, 64>());
   chain(set_smem<128, 16>());
   chain(set_smem<128, 64>());
   chain(set_smem<256, 16>());
   chain(set_smem<256, 64>());
-  chain(configure_attention_tc());
+  chain(configure_attention_tc(dev));
   chain(configure_attention_decode());
   return e;
 }
@@ -733,8 +736,8 @@ cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st) {
   return c.D == 64 ? launch_all<64>(c, st) : c.D == 128 ? launch_all<128>(c, st) : launch_all<256>(c, st);
 }
 
-cudaError_t run_attention(AttnCall& c, int num_sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
-  c.plan = plan_attention(c, num_sms);
+cudaError_t run_attention(AttnCall& c, const AttnDevice& dev, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  c.plan = plan_attention(c, dev);
   // fewer ranges where the caller's workspace holds no more parts
   while (attention_workspace(c) > workspace_bytes && (c.plan.ns > 1 || c.plan.ne > 1)) {
     int& n = c.plan.ns > c.plan.ne ? c.plan.ns : c.plan.ne;

@@ -13,7 +13,8 @@
 using namespace rtv;
 
 struct rtv_ops {
-  int device = 0, num_sms = 0;
+  int device = 0;
+  AttnDevice attn{};
   unsigned* status = nullptr;
   std::string last_error;
 };
@@ -204,7 +205,7 @@ rtv_status attention_shape(rtv_ops* h, const rtv_queries* q, const rtv_kv* pre, 
   };
   source(pre, &c->pre, &c->pre_f8);
   source(own, &c->own, &c->own_f8);
-  if (rows > 0) c->plan = plan_attention(*c, h->num_sms);
+  if (rows > 0) c->plan = plan_attention(*c, h->attn);
   return RTV_OK;
 }
 
@@ -280,8 +281,7 @@ rtv_status rtv_ops_create(int cuda_device, rtv_ops** out) {
   if (!h) return RTV_ERR_OOM;
   h->device = cuda_device;
   DeviceGuard dg(cuda_device);
-  cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cuda_device);
-  if (e == cudaSuccess) e = configure_attention();
+  cudaError_t e = configure_attention(&h->attn);
   if (e == cudaSuccess) e = cudaMalloc(&h->status, sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(unsigned));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();

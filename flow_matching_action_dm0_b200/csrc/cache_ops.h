@@ -64,27 +64,33 @@ struct AttnCall {
   long long timeout_ns;
 };
 
+constexpr int kMaxCluster = 8;
+// What a plan needs to know of a GPU.  Each handle holds its own, filled when
+// it is made, so that a call's split (and workspace, and the order of its
+// sums) depends on its shape and its GPU alone.
+struct AttnDevice {
+  int num_sms;
+  int at_once[3][kMaxCluster + 1];   // [head_dim 64, 128, 256][ranks]: CTAs of the tensor-core kernel that run at once in clusters
+};
+// Sets the kernels' attributes on the current device (outside any capture) and describes it.
+cudaError_t configure_attention(AttnDevice* dev);
 // Chooses the split for a call whose shape fields are set.
-AttnPlan plan_attention(const AttnCall& c, int num_sms);
+AttnPlan plan_attention(const AttnCall& c, const AttnDevice& dev);
 // Bytes of the partial results of a planned call.
 size_t attention_workspace(const AttnCall& c);
 // Enqueues a planned call; workspace as above.
 cudaError_t launch_attention(AttnCall& c, void* workspace, cudaStream_t st);
 // Plans and enqueues a call whose workspace is given; makes fewer ranges of the keys where it is too small.
-cudaError_t run_attention(AttnCall& c, int num_sms, void* workspace, size_t workspace_bytes, cudaStream_t st);
-// Sets the kernels' attributes on the current device (outside any capture).
-cudaError_t configure_attention();
+cudaError_t run_attention(AttnCall& c, const AttnDevice& dev, void* workspace, size_t workspace_bytes, cudaStream_t st);
 // The tensor-core kernel (bf16 queries).
-cudaError_t configure_attention_tc();
+cudaError_t configure_attention_tc(AttnDevice* dev);
 cudaError_t launch_attention_tc(const AttnCall& c, cudaStream_t st);
 int attention_tc_rows(int D);   // rows of a CTA
 constexpr int attention_tc_keys(int D) { return D == 256 ? 64 : 128; }   // keys of a tile
-int attention_tc_at_once(int D, int ranks);   // CTAs that run at once in clusters of `ranks` (0: unknown)
 // The few-row kernel (bf16 queries, 16 rows of an element or less).
 cudaError_t configure_attention_decode();
 cudaError_t launch_attention_decode(const AttnCall& c, cudaStream_t st);
 constexpr int kDecodeRows = 16;
-constexpr int kMaxCluster = 8;
 constexpr int decode_groups(int D) { return D == 256 ? 6 : 4; }                          // of 16 keys each, in a tile
 constexpr int attention_decode_ctas(int D) { return D == 256 ? 1 : D == 128 ? 3 : 4; }   // CTAs of an SM
 

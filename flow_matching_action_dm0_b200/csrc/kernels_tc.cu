@@ -1631,6 +1631,7 @@ struct FastPath {
   // indexes the same storage as [Gmax][Hq/2][16][128][D]) and their (max, sum)
   __nv_bfloat16* att_po = nullptr;
   size_t att_po_bytes = 0;
+  AttnDevice attn_dev{};   // for the operators over caches
   float* att_pml = nullptr;
   // tensor-core attention (head pairs sharing a KV head): tiled operands
   bool tc_attn = false;
@@ -1921,15 +1922,17 @@ rtv_status fast_create(rtv_ctx* ctx) {
                         k.mlp_dim % 128 == 0 && (ctx->Q % 128) == 0 && S <= 64 && step_ok && n_mma_max > 0;
   if (!shape_ok) return RTV_OK;
   int dev = ctx->device;
+  AttnDevice attn_dev;
   if (configure_gemm<GM_QKV>() != cudaSuccess || configure_gemm<GM_O>() != cudaSuccess ||
       configure_gemm<GM_GU>() != cudaSuccess || configure_gemm<GM_DOWN>() != cudaSuccess ||
       configure_attn<128>() != cudaSuccess || configure_attn<256>() != cudaSuccess ||
       configure_attn_tc<128>() != cudaSuccess || configure_attn_tc<256>() != cudaSuccess ||
-      configure_attention() != cudaSuccess) {
+      configure_attention(&attn_dev) != cudaSuccess) {
     cudaGetLastError();
     return RTV_ERR_CUDA;
   }
   FastPath* fp = new FastPath();
+  fp->attn_dev = attn_dev;
   cudaDeviceGetAttribute(&fp->num_sms, cudaDevAttrMultiProcessorCount, dev);
   // A bare block's GEMMs leave no room for a partner kernel: two CTAs per SM
   // may take half of the SM's 228 KB each (less the per-CTA reservation and
@@ -2440,7 +2443,7 @@ rtv_status fast_prefill(rtv_ctx* pre, rtv_ctx* ex, const __nv_bfloat16* emb, int
       c.own.len = P;
       c.status = pre->status;
       c.timeout_ns = k.barrier_timeout_ns;
-      e = run_attention(c, fp->num_sms, fp->att_po, fp->att_po_bytes, st);
+      e = run_attention(c, fp->attn_dev, fp->att_po, fp->att_po_bytes, st);
     } else if (e == cudaSuccess)
       e = D == 256 ? launch_attn_tc<256>(atc, ntp + 1, G, fp->num_sms, st)
                    : launch_attn_tc<128>(atc, ntp + 1, G, fp->num_sms, st);
@@ -2700,7 +2703,7 @@ rtv_status layers_impl(rtv_ctx* ctx, int G, int P, int prefix_batch_stride, cons
       c.own.len = S;
       c.status = ctx->status;
       c.timeout_ns = k.barrier_timeout_ns;
-      if (e == cudaSuccess) e = run_attention(c, fp->num_sms, fp->att_po, fp->att_po_bytes, st);
+      if (e == cudaSuccess) e = run_attention(c, fp->attn_dev, fp->att_po, fp->att_po_bytes, st);
     } else {
       at.trace = tr(l, 4);
       at.pk = (const __nv_bfloat16*)ctx->prefix_kv + (size_t)(2 * l) * kv_layer;
