@@ -93,6 +93,8 @@ rtv_status rtv_set_prefix_kv_quantized(rtv_ctx* ctx, const void* codes, const fl
   const cudaError_t e = rtv::launch_kv_read(describe(ctx, const_cast<void*>(codes), const_cast<float*>(scales), prefix_len, batch),
                                             (cudaStream_t)stream);
   if (e != cudaSuccess) return sfail(ctx, RTV_ERR_CUDA, std::string("prefix read: ") + cudaGetErrorString(e));
+  // The rows are the new prefix's from here on: until the tiles are too, no call may read either.
+  ctx->have_prefix = false;
   if (ctx->use_fast) s = rtv::fast_prefix_update(ctx, batch, prefix_len, (cudaStream_t)stream);
   if (s != RTV_OK) return s;
   ctx->prefix_len = prefix_len;

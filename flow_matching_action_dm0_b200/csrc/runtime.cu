@@ -621,6 +621,8 @@ rtv_status rtv_set_prefix_kv(rtv_ctx* ctx, const void* kv, int prefix_len, int b
     launch_prefix_pack<__nv_bfloat16>((const __nv_bfloat16*)src, (__nv_bfloat16*)ctx->prefix_kv, k.n_layers, batch,
                                       prefix_len, k.n_kv_heads, k.head_dim, k.max_batch, k.max_prefix_len, st);
   CK(cudaGetLastError());
+  // The rows are the new prefix's from here on: until the tiles are too, no call may read either.
+  ctx->have_prefix = false;
   if (tmp) CK(cudaFreeAsync(tmp, st));
   if (ctx->use_fast) {
     const rtv_status fs = fast_prefix_update(ctx, batch, prefix_len, st);

@@ -165,7 +165,8 @@ rtv_status rtv_load_expert(rtv_ctx* ctx, const rtv_tensor* params, int n_params)
  * [n_layers][2][batch][prefix_len][n_kv_heads][head_dim] in the config dtype
  * (index 0 = keys, already rotated; 1 = values).  It is copied on `stream`
  * into library-owned memory of fixed address (the static-address contract
- * of [DM0.5] 6.5).  prefix_len <= max_prefix_len, batch <= max_batch. */
+ * of [DM0.5] 6.5).  prefix_len <= max_prefix_len, batch <= max_batch.  A call
+ * that fails once the copy is enqueued leaves no prefix (RTV_ERR_STATE). */
 rtv_status rtv_set_prefix_kv(rtv_ctx* ctx, const void* kv, int prefix_len, int batch, rtv_stream stream);
 
 /* Install the prefix KV cache without allocating any device memory.  No
