@@ -381,11 +381,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, attention_decode_ctas(D)
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     const int row = n + 8 * r;
     if (F8) {
-      const float f = m[r] == -INFINITY ? 1.f : ex2(mv[r] - kUp - m[r]);
+      // (in two steps: with value scales below 2^-119 the whole factor is less than the least normal number, and ex2 gives 0)
+      const float f = m[r] == -INFINITY ? 1.f : ex2(0.5f * (mv[r] - kUp - m[r]));
 #pragma unroll
       for (int j = 0; j < NI * 8; ++j) {
-        o[j][2 * r] *= f;
-        o[j][2 * r + 1] *= f;
+        o[j][2 * r] = o[j][2 * r] * f * f;
+        o[j][2 * r + 1] = o[j][2 * r + 1] * f * f;
       }
     }
     // a NaN sum counts with every weight, a sum of 0 (nothing seen) with none

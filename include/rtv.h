@@ -520,14 +520,16 @@ rtv_status rtv_kv_read(rtv_ops* ops, const rtv_kv* cache, int first, const int* 
  * in the queries' dtype or RTV_FP8_E4M3.  What hidden keys and values hold is
  * never used, NaN and infinities included.  bf16 queries: products on the
  * tensor cores with fp32 sums, softmax weights rounded to bf16; fp32 queries:
- * fp32 throughout.  bf16 queries over E4M3: up to 16 rows (query tokens x
- * query heads of a key/value head) take the codes as they are, with weight x
- * value scale rounded to f16 (2^-11 of each, and 2^-32 of the row's largest);
- * more rows, and a prefix that several elements share or that has own keys
- * beside it, are read back to bf16 in the workspace first, so it grows with
- * the cache.  workspace: at least rtv_cross_attention_workspace bytes,
- * 256-byte aligned (NULL when that is 0), in use until the call's work is
- * done. */
+ * fp32 throughout.  A row's weighted sum of values is held in fp32, with
+ * weights of up to 2^8 for bf16 queries: values whose number times magnitude
+ * passes 2^119 may overflow it.  bf16 queries over E4M3: up to 16 rows (query
+ * tokens x query heads of a key/value head) take the codes as they are, with
+ * weight x value scale rounded to f16 (2^-11 of each, and 2^-32 of the row's
+ * largest); more rows, and a prefix that several elements share or that has
+ * own keys beside it, are read back to bf16 in the workspace first, so it
+ * grows with the cache.  workspace: at least rtv_cross_attention_workspace
+ * bytes, 256-byte aligned (NULL when that is 0), in use until the call's work
+ * is done. */
 rtv_status rtv_cross_attention(rtv_ops* ops, const rtv_queries* q, const rtv_kv* kv, const int* lens,
                                const unsigned char* mask, long long mask_stride, void* workspace,
                                size_t workspace_bytes, rtv_stream stream);

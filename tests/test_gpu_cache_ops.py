@@ -623,3 +623,25 @@ def test_a_nan_in_one_key_range_reaches_its_rows_alone(ops):
     out, lse = ops.cross_attention(q, (k, v), lens=ints([1000, 900]), lse=True)
     bad = torch.isnan(out).any(-1)
     assert bad[0, 5, 3] and bad.sum() == 1 and torch.isnan(lse[0, 5, 3]) and torch.isfinite(lse).sum() == lse.numel() - 1
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("tq", [2, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_near_the_least_exponents(ops, dtype, cache, tq, d):
+    """Values of 2^-112 (E4M3 scales of 2^-120) weigh like any others: 2^112 times them is compared.  The results'
+    step near 2^-126 (2^-134 at most) is under 2^-6 of the bound, 2^-8 times the mean of |v|."""
+    g = gen(35 + d + tq)
+    b, n, shrink = 2, 700, 2.0 ** -112
+    q, k = rand(g, b, tq, 8, d, dtype=dtype), rand(g, b, n, 2, d, dtype=dtype)
+    v = ((torch.rand((b, n, 2, d), generator=g, device=DEV) * 2 - 1) * shrink).to(T[dtype])
+    kv = (k, v)
+    if cache == "fp8":
+        kv = empty_cache(b, n, 2, d)
+        ops.write(kv, k, v)
+        assert float(kv.v_scale.max()) <= 2.0 ** -120
+        k, v = ops.read(kv, dtype="f32")
+    lens = [n, 33]
+    out, lse = ops.cross_attention(q, kv, lens=ints(lens), lse=True)
+    kn, vn = f64(k), f64(v) / shrink
+    check_attention(q, lambda i: [(kn[i], vn[i], visible(n, lens, None, i))], d ** -0.5, out.double() / shrink, lse)
