@@ -114,6 +114,8 @@ rtv_status check_kv_memory(rtv_ops* h, const rtv_kv* a, const std::string& what,
                      a->token_stride, a->n_heads, a->head_stride));
   // rows of one call's source may be shared between elements and heads, not between tokens
   if (a->n_tokens > 1 && a->token_stride == 0) return ofail(h, RTV_ERR_ARG, what + ": token stride 0");
+  if (written && (a->k == a->v || (a->dtype == RTV_FP8_E4M3 && a->k_scale == a->v_scale)))
+    return ofail(h, RTV_ERR_ARG, what + ": keys and values are written to the same place");
   if (a->dtype != RTV_FP8_E4M3) return RTV_OK;
   OTRY(check_ptr(h, a->k_scale, (what + " k_scale").c_str(), 4));
   OTRY(check_ptr(h, a->v_scale, (what + " v_scale").c_str(), 4));

@@ -443,9 +443,9 @@ void rtv_prefill_destroy(rtv_prefill* p);
  * CUDA graph and run on several streams at once, as long as each has a
  * workspace of its own; calls on one handle must not run concurrently from
  * several host threads, and a captured call is not replayed after
- * rtv_ops_destroy.  Outputs must not overlap inputs, nor the rows of an
- * output each other (RTV_ERR_ARG unless each stride steps over all that the
- * smaller ones reach).
+ * rtv_ops_destroy.  Outputs must not overlap inputs or each other
+ * (keys and values of one address: RTV_ERR_ARG), nor the rows of an output
+ * (RTV_ERR_ARG unless each stride steps over all that the smaller ones reach).
  * ------------------------------------------------------------------------ */
 typedef struct rtv_ops rtv_ops;
 
