@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   using C = Cfg<D>;
   constexpr int NC = C::NC, NST = C::NST, VK = C::VK, KT = C::KT;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_loads;                // a wait has run out; loads issued
   uint8_t* Qs = (uint8_t*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = Qs + C::MT * C::QB;
   uint64_t* ready = (uint64_t*)(Qs + C::kOff);    // [NST] the stage holds its operand
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform)
   if (tid == 0) {
-    s_abort = 0;
+    s_abort = s_loads = 0;
     for (int i = 0; i < NST; ++i) {
       ptx::mbar_init(&ready[i], 1);
       ptx::mbar_init(&empty[i], 1);
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (lane == 0) {
       const int pre_h = u.kvh * maps.pre_h, own_h = u.kvh * maps.own_h, own_b = u.b * maps.own_b;
       bool ok = true;
-      int s = 0, ph = 1;
+      int s = 0, ph = 1, loads = 0;
       for (int i = 0; i < 2 * n && ok; ++i) {
         if (C::kQInTmem && i == kFirst) {   // (Q passes through the ring's other stages)
           ok = wait(&q_ready[0], 0);
@@ -338,9 +338,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           // a K stage is CK chunks of 64 dims of the tile's keys, a V stage all dims of VK keys
           if (o & 1) tma_load(ring + s * kStage, map, t.k0 + cc * VK, 0, h, b, &ready[s]);
           else tma_load(ring + s * kStage, map, t.k0, cc * C::CK, h, b, &ready[s]);
+          ++loads;
           if (++s == NST) s = 0, ph ^= 1;
         }
       }
+      s_loads = loads;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -765,10 +767,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (s_abort) {   // after a timeout loads may be in flight: give them time to land before the CTA's memory is reused
-    const uint64_t t0 = ptx::globaltimer();
-    while (ptx::globaltimer() - t0 < 2000000ull) {
-    }
+  if (s_abort) {   // after a timeout loads may be in flight: they land before the CTA's memory is another's
+    if (tid == 0)
+      for (int i = max(s_loads - NST, 0); i < s_loads; ++i)
+        if (!ptx::mbar_wait(&ready[i % NST], (uint32_t)(i / NST) & 1u, kDrainNs)) atomicOr(c.status, RTV_DEV_TIMEOUT);
+    __syncthreads();
   }
   if (warp == 1) {
     ptx::tc_fence_after();

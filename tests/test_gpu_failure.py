@@ -72,3 +72,32 @@ def test_wait_that_runs_out_is_reported_and_the_context_stays_usable(cuda_ok, mo
     ok.close()
     ref = O.denoise(O.to_f64(weights), cfg, noise, state, make_prefix_kv(cfg), 2)
     assert bf16_tolerance_ok(got, ref), rel_l2(got, ref)
+
+
+def test_shared_prefix_attention_wait_that_runs_out_is_reported(cuda_ok):
+    """rtv_denoise_shared's attention (and the projections beside it) with a
+    wait limit of one nanosecond: loads and products in flight are drained, the
+    status tells, and the GPU computes correctly afterwards."""
+    cfg = get_config("pi0-bf16", n_layers=1, prefix_len=700)     # several key ranges, joined in clusters
+    weights = make_weights(cfg)
+    kv = np.ascontiguousarray(f32_to_bf16_bits(make_prefix_kv(cfg)))
+    noise, state = np.ascontiguousarray(make_noise(cfg, batch=3)), make_state(cfg)[0]
+    for n in (1, 3):
+        ex = ActionExpert(cfg, max_batch=3, barrier_timeout_ns=1)
+        ex.load(weights)
+        ex.set_prefix_kv(kv)
+        for _ in range(2):
+            ex.denoise_shared(noise[:n], state, 2)
+            s, bits = L.rtv_device_status(ex.h)
+            assert s == L.RTV_ERR_TIMEOUT and (bits & L.RTV_DEV_TIMEOUT), (s, bits)
+        ex.close()
+    ok = ActionExpert(cfg, max_batch=3)
+    ok.load(weights)
+    ok.set_prefix_kv(kv)
+    got = ok.denoise_shared(noise, state, 2)
+    assert ok.status() == (0, 0)
+    ok.close()
+    W = O.to_f64(weights)
+    for i in range(3):
+        ref = O.denoise(W, cfg, noise[i:i + 1], state[None], make_prefix_kv(cfg), 2)
+        assert bf16_tolerance_ok(got[i:i + 1], ref), rel_l2(got[i:i + 1], ref)
