@@ -228,3 +228,24 @@ def test_park_and_install_on_a_stream_of_their_own(cuda_ok):
         assert bf16_tolerance_ok(shared.cpu().numpy(), want.cpu().numpy(), rel=2e-2, abs_=6e-2)
     assert ex.status() == (0, 0)
     ex.close()
+
+
+@pytest.mark.parametrize("n_tokens,heads", [(961, 8), (1025, 4)])
+def test_prefill_past_the_tiled_attention_with_more_heads_on_one(cuda_ok, n_tokens, heads):
+    from flow_matching_action_dm0_b200 import ActionExpert, PrefillStack
+    cfg = get_config("pi0-bf16", n_layers=2, prefix_len=n_tokens)
+    pc = get_prefill_config("gemma2b-prefill", n_layers=2, width=512, n_q_heads=heads, mlp_dim=1024, n_tokens=n_tokens)
+    W = make_weights(cfg)
+    ex = ActionExpert(cfg, max_batch=1, max_prefix_len=n_tokens)
+    ex.load(W)
+    pf = PrefillStack(pc, max_tokens=n_tokens + 70)
+    pf.load({k: f32_to_bf16_bits(v) if v.ndim == 2 else v
+             for i in range(2) for k, v in make_prefill_weights(pc, layers=[i]).items()})
+    emb = make_prefix_embeddings(pc, n_tokens=n_tokens)
+    noise, state = make_noise(cfg), make_state(cfg)
+    got = pf.denoise(ex, emb, noise[0], state[0], 2)
+    ref = OP.prefill_denoise(lambda i: make_prefill_weights(pc, layers=[i]), pc, W, cfg, emb, noise, state, 2)[0]
+    assert bf16_tolerance_ok(got, ref), (rel_l2(got, ref), np.max(np.abs(got - ref)))
+    assert pf.status() == (0, 0) and ex.status() == (0, 0)
+    pf.close()
+    ex.close()
