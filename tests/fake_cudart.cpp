@@ -16,12 +16,14 @@ struct Gpu {
 Gpu g_gpu[4];
 int g_gpus = 1, g_current = 0;
 long g_launches = 0, g_fails_at = 0;          // the launch that fails, counted from now (0: none)
+int g_launched_on = -1;                       // the current GPU of the last launch
 std::map<char*, std::pair<size_t, int>> g_memory;   // address -> bytes, GPU
 cudaError_t g_last = cudaSuccess;
 
 cudaError_t done(cudaError_t e) { return e == cudaSuccess ? e : g_last = e; }
 cudaError_t launch() {
   ++g_launches;
+  g_launched_on = g_current;
   return done(g_fails_at && --g_fails_at == 0 ? cudaErrorLaunchOutOfResources : cudaSuccess);
 }
 int encode_tensor_map() { return 0; }
@@ -38,6 +40,7 @@ void fake_gpus(int n) {
 void fake_clusters(int gpu, int size, int n) { g_gpu[gpu].clusters_of[size] = n; }
 void fake_fail_launch(long nth) { g_fails_at = nth; }
 long fake_launches() { return g_launches; }
+int fake_launched_on() { return g_launched_on; }
 
 cudaError_t cudaGetDeviceCount(int* n) { return *n = g_gpus, cudaSuccess; }
 cudaError_t cudaGetDevice(int* d) { return *d = g_current, cudaSuccess; }

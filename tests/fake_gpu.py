@@ -40,4 +40,5 @@ def gpus(host_library_path, monkeypatch):
     monkeypatch.setattr(L, "_lib", None)
     lib = L.load_library(host_library_path)
     lib.fake_gpus(2)
+    lib.cudaSetDevice(0)
     return lib

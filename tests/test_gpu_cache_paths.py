@@ -249,3 +249,33 @@ def test_prefill_past_the_tiled_attention_with_more_heads_on_one(cuda_ok, n_toke
     assert pf.status() == (0, 0) and ex.status() == (0, 0)
     pf.close()
     ex.close()
+
+
+def test_a_captured_park_and_install_replay_on_new_values(cuda_ok):
+    cfg = get_config("pi0-bf16", n_layers=2, prefix_len=90)
+    ex, W, kv = expert(cfg, 1)
+    noise, state = np.ascontiguousarray(make_noise(cfg)), np.ascontiguousarray(make_state(cfg))
+    first = ex.get_prefix_kv_quantized(cfg.prefix_len)
+    ex.set_prefix_kv(np.ascontiguousarray(make_prefix_kv(cfg, seed=9)))
+    second = ex.get_prefix_kv_quantized(cfg.prefix_len)
+    want = []
+    for pair in (first, second):
+        ex.set_prefix_kv_quantized(*pair)
+        want.append(ex.denoise(noise, state, 2))
+    given = [t.clone() for t in first]
+    ex.set_prefix_kv_quantized(*given)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ex.set_prefix_kv_quantized(*given)
+        parked = ex.get_prefix_kv_quantized(cfg.prefix_len)
+    for i in (1, 0, 1):
+        for t, new in zip(given, (first, second)[i]):
+            t.view(torch.uint8).copy_(new.view(torch.uint8))
+        graph.replay()
+        np.testing.assert_array_equal(ex.denoise(noise, state, 2), want[i])
+        values = [(c.double() * s.double()[..., None]) for c, s in (given, parked)]
+        assert bool(torch.equal(*values))          # the same values (a code's scale may be half as large)
+    assert ex.status() == (0, 0)
+    del graph
+    ex.close()
