@@ -6,7 +6,8 @@ bandwidth it achieves.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
     python bench.py --workload flash-draft      # the FLASH draft model alone
-    python bench.py --workload gemma2b-prefill  # VLM prefill + the pi0-bf16 chunk, one graph
+    python bench.py --workload gemma2b-prefill  # VLM prefill + the pi0-bf16 chunk, one graph (--tokens N: longer)
+    python bench.py --workload candidate-chunks # chunks over one prefix against a prefix each; parking a prefix
 
 One "step" is one call of rtv_denoise: the whole hot path (10 Euler steps
 through the expert) over one batch of synthetic input.  With N > 1 the
@@ -43,6 +44,8 @@ sys.path.insert(0, ROOT)
 METRIC = "10-step action-chunk latency (us) and achieved HBM GB/s vs 8 TB/s roofline"
 PREFILL_METRIC = ("prefill + 10-step chunk latency (us): Gemma-2B-class prefill over 816 tokens writing the "
                   "KV cache, then the pi0-bf16 chunk, one CUDA graph")
+CANDIDATE_METRIC = ("latency (us) of 16 candidate chunks of 10 steps over one 816-token prefix (rtv_denoise_shared, "
+                    "pi0-bf16)")
 DRAFT_METRIC = "FLASH draft forward latency (us): one Gemma-2B-width block + action head over 768 image tokens"
 # Earlier measurements on this machine's B200s, used only when MEASURED_PEAKS.json is absent: a STREAM-style
 # copy, and a cuBLAS bf16 GEMM as a burst and as a seconds-long loop under the power cap.
@@ -59,6 +62,7 @@ def parse_args(argv=None):
     ap.add_argument("--n-steps", type=int, default=10, help="Euler steps per chunk")
     ap.add_argument("--batch", type=int, default=0,
                     help="independent chunks per call, each with its own prefix (default: the workload's)")
+    ap.add_argument("--tokens", type=int, default=0, help="override the prefill workload's token count")
     ap.add_argument("--layers", type=int, default=0,
                     help="override the workload's layer count (profiling runs on smaller captures only; "
                          "the JSON line then names the reduced depth)")
@@ -307,6 +311,9 @@ def run_reference(args, info):
     from synthetic import DRAFTS, PREFILLS
     if args.workload in DRAFTS:
         run_reference_draft(args, info)
+        return
+    if args.workload == "candidate-chunks":
+        print(json.dumps({"impl": "reference", "unavailable": "the oracle denoises one chunk at a time"}), flush=True)
         return
     if args.workload in PREFILLS:
         run_reference_prefill(args, info)
@@ -747,6 +754,8 @@ def run_prefill(args, info):
     dev = info.local_rank
     torch.cuda.set_device(dev)
     pc = get_prefill_config(args.workload)
+    if args.tokens > 0:
+        pc = pc.with_(n_tokens=args.tokens)
     cfg = get_config("pi0-bf16", n_steps=args.n_steps, prefix_len=pc.n_tokens)
     if args.layers > 0:
         pc = pc.with_(n_layers=args.layers)
@@ -853,6 +862,87 @@ def run_prefill(args, info):
     print(json.dumps(line), flush=True)
 
 
+def run_candidates(args, info):
+    """Candidate chunks of one observation (rtv_denoise_shared) beside the same
+    number of chunks with a prefix each (rtv_denoise), and the prefix parked
+    in E4M3 and installed again; medians of K calls, one at a time."""
+    import torch
+
+    from flow_matching_action_dm0_b200 import ActionExpert
+    from flow_matching_action_dm0_b200 import replicas as R
+    from synthetic import f32_to_bf16_bits, get_config, make_noise, make_prefix_kv, make_state, make_weights
+
+    dev = info.local_rank
+    torch.cuda.set_device(dev)
+    cfg = get_config("pi0-bf16", n_steps=args.n_steps)
+    if args.layers > 0:
+        cfg = cfg.with_(n_layers=args.layers)
+    n, K, counts = cfg.n_steps, args.steps, (1, 2, 4, 8, 16)
+    weights = make_weights(cfg)
+    one = torch.from_numpy(f32_to_bf16_bits(make_prefix_kv(cfg)).view(np.int16)).view(torch.bfloat16).cuda(dev)
+    noise = torch.from_numpy(make_noise(cfg, batch=counts[-1]))
+    state = torch.from_numpy(make_state(cfg, batch=1)).expand(counts[-1], -1).contiguous()
+    stream = torch.cuda.Stream(dev)
+    uuid = str(torch.cuda.get_device_properties(dev).uuid)
+    gpu_id = uuid if uuid.startswith("GPU-") else "GPU-" + uuid
+
+    def us(call):
+        for _ in range(max(3, args.warmup)):
+            call()
+        times = []
+        for _ in range(K):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record(stream)
+            call()
+            b.record(stream)
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return R.max_over_ranks(statistics.median(times), info, dev) * 1000.0
+
+    rows, parked_bytes = {}, 0
+    with ClockSampler(gpu_id) as clk:
+        for c in counts:
+            ex = ActionExpert(cfg, device=dev, max_batch=c, max_taus=4)
+            ex.load(weights)
+            noise_d, state_d = noise[:c].cuda(dev), state[:c].cuda(dev)
+            out_d = torch.empty_like(noise_d)
+            torch.cuda.synchronize(dev)
+            ex.set_prefix_kv(one.expand(-1, -1, c, -1, -1, -1).contiguous(), stream=stream)
+            torch.cuda.synchronize(dev)
+            each = us(lambda: ex.denoise(noise_d, state_d, n, out_d, stream=stream))
+            ex.set_prefix_kv(one, stream=stream)
+            shared = us(lambda: ex.denoise_shared(noise_d, state_d[0], n, out_d, stream=stream))
+            rows[str(c)] = {"shared_us": shared, "prefix_each_us": each}
+            if c == counts[-1]:
+                parked = ex.get_prefix_kv_quantized(cfg.prefix_len, stream=stream)
+                park = us(lambda: ex.get_prefix_kv_quantized(cfg.prefix_len, stream=stream))
+                install = us(lambda: ex.set_prefix_kv_quantized(*parked, stream=stream))
+                parked_bytes = sum(t.numel() * t.element_size() for t in parked)
+                noise_h, state_h = noise.pin_memory(), state[0].contiguous().pin_memory()
+                out_h = torch.empty_like(noise_h).pin_memory()
+                e2e = us(lambda: ex.denoise_shared(noise_h, state_h, n, out_h, stream=stream))
+            s, bits = ex.status()
+            if s != 0:
+                raise RuntimeError(f"device status {bits:#x} after the timed region")
+            ex.close()
+    if not info.is_main:
+        return
+    value = rows[str(counts[-1])]["shared_us"]
+    print(json.dumps({
+        "metric": CANDIDATE_METRIC, "value": value, "unit": "us", "n_gpus": info.world, "steps": K,
+        "warmup": max(3, args.warmup), "ms_per_step": value / 1000.0, "higher_is_better": False, "scaling": "weak",
+        "vs_baseline": None, "dtype": cfg.dtype, "data": "synthetic",
+        "config": {"workload": args.workload, "expert": "pi0-bf16", "layers": cfg.n_layers, "chunks": counts[-1],
+                   "n_steps": n, "prefix_len": cfg.prefix_len, "parallelism": f"replicas x{info.world}",
+                   "l2": "inputs larger than L2: 623 MB of weights stream from HBM every step; no flush"},
+        "candidates": rows,
+        "park_us": park, "install_us": install, "prefix_bytes": one.numel() * 2, "parked_bytes": parked_bytes,
+        "e2e": {"value": e2e, "unit": "us", "h2d_bytes_per_step": int(4 * (noise.numel() + state[0].numel())),
+                "d2h_bytes_per_step": int(4 * noise.numel())},
+        "clocks": clk.summary(),
+    }), flush=True)
+
+
 def run_trace(args):
     """One traced chunk: the library prints per-CTA phase stamps (globaltimer)
     of the projections and the attention of layer 0, first Euler step."""
@@ -888,6 +978,8 @@ def main(argv=None):
             run_draft(args, info)
         elif args.workload in PREFILLS:
             run_prefill(args, info)
+        elif args.workload == "candidate-chunks":
+            run_candidates(args, info)
         else:
             run_ours(args, info)
     finally:
