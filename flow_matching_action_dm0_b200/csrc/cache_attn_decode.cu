@@ -26,9 +26,10 @@
 // end, in order.
 //
 // Measured on B200 (cold L2): 32 single tokens, 8 heads on 2, over E4M3
-// caches of up to 16,384 tokens of 128 dims (210 MB), 64 us, 3.3 TB/s: the
-// conversions of the codes and the longest of the sequences, not the memory,
-// hold it.  One token, 8 heads on one, over 816 tokens of 256 dims: 12 us, not
+// caches of up to 16,384 tokens of 128 dims (210 MB), 64 us, 3.3 TB/s; with
+// all of them that long (268 MB) 78 us.  The conversions of the codes hold it,
+// and with lengths that differ the longest sequences, whose keys are split
+// over as many CTAs as the shortest's.  One token, 8 heads on one, over 816 tokens of 256 dims: 12 us, not
 // much more than the host takes for the call.
 
 #include "cache_ops.h"

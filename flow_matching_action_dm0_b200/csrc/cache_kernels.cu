@@ -31,10 +31,12 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // codes = E4M3(x * 2^-e) (exact product, one rounding).  A row is D/8 lanes
 // of 8 elements; the maximum over the row's magnitudes is taken on their bit
 // patterns, which order like the values with infinities and NaN on top.
-// Bound by its bytes (bf16 read, codes written, a scale a row): four rows'
-// loads in flight a thread (one: 92 us), past L1 as nothing is read twice.
-// Measured on B200: 64 x 816 tokens x 8 heads x 128, 245 MB in 57 us, 4.3
-// TB/s (a copy reaches 6.6; some of the sequences are short).
+// Four rows' loads are in flight a thread (one: 92 us), past L1 as nothing is
+// read twice.  Measured on B200: 64 x 816 tokens x 8 heads x 128, bf16, 57 us
+// for 245 MB (some sequences short) and 72 us for the whole 324 MB, 4.3-4.5
+// TB/s where a copy reaches 6.6.  What holds it is the instructions, not the
+// memory: issue slots are 82% in use, DRAM 46%.  fp32 rows bring twice the
+// bytes to the same work and reach 6.7 TB/s (538 MB in 80 us).
 // ---------------------------------------------------------------------------
 constexpr int kRowsAhead = 4;                   // rows whose loads a thread has in flight
 
@@ -112,8 +114,8 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const __grid_constant__ C
 }
 
 // Cache read: code * scale in fp32, rounded to T.  A row is D/16 lanes of 16
-// codes, 32 bytes of bf16 a lane.  Bound by its bytes as the write is: 72 x
-// 816 tokens x 4 heads, 333 MB in 65 us, 5.1 TB/s.
+// codes, 32 bytes of bf16 a lane.  72 x 816 tokens x 4 heads of 256 dims, 333
+// MB in 65 us, 5.1 TB/s: warps wait for their loads (issue slots 48% in use).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ CacheCall c) {
   constexpr int LPR = D / 16;
@@ -591,7 +593,11 @@ AttnPlan plan_attention(const AttnCall& c, const AttnDevice& dev) {
   const bool stack = c.pre.len > 0 && c.B > 1 && p.rows_b <= (c.bf16 ? 64 : 16);
   p.prefix_in_elem = c.pre.len > 0 && !stack;
   // E4M3: the few-row kernel reads one source of codes itself; the others are
-  // read back to bf16 first, once for all of the rows that go over them.
+  // read back to bf16 first, once for all of the rows that go over them, by a
+  // launch that moves five times the codes' bytes.  (Measured on B200, 32
+  // caches of 16384 tokens x 2 heads x 128: 16 rows from the codes 80 us, 20
+  // rows read back first 250, where bf16 caches take 113 and 104.  One prefix
+  // of 8192 tokens for 64 single tokens with own keys: 33 us, in bf16 28.)
   const bool codes = p.decode && !stack && (!c.pre.len || !c.own.len);
   p.unpack_pre = c.bf16 && c.pre.len > 0 && c.pre_f8 && !codes;
   p.unpack_own = c.bf16 && c.own.len > 0 && c.own_f8 && !codes;

@@ -208,8 +208,10 @@ rtv_status rtv_denoise(rtv_ctx* ctx, const float* noise, const float* state, int
  * [n_chunks][H][A]; n_chunks <= max_batch.  The tensor-core path with the
  * bidirectional mask reads the prefix through the shared-prefix attention
  * (rtv_shared_attention's kernels); results agree with rtv_denoise's on
- * copied prefixes to the paths' rounding.  Graphs, pointers and errors as
- * for rtv_denoise. */
+ * copied prefixes to the paths' rounding.  It reads the prefix once for all
+ * chunks and spares its copies, not the context's memory (max_batch prefixes
+ * are allocated either way); for one or two chunks rtv_denoise is the faster
+ * call.  Graphs, pointers and errors as for rtv_denoise. */
 rtv_status rtv_denoise_shared(rtv_ctx* ctx, const float* noise, const float* state, int n_chunks, int n_steps,
                               float* actions_out, rtv_stream stream);
 
