@@ -102,8 +102,8 @@ def algorithmic_bytes_per_step(cfg, batch=1):
 # launches of a chunk with the L2 carried between kernels (profiles/dram_traffic_pi0-bf16_full_depth.md).  The
 # figure holds for the kernel sources it was taken on, identified by their SHA-256; after any change to them the
 # bench reports null until the capture is taken again.
-TRAFFIC_PI0_BF16 = {"bytes_per_chunk": 6450270720,
-                    "kernel_sources_sha256": "11ee4518394dc49b6a90be934d28628fc2e1e1626e4b6a3e7c5607ee7922f136"}
+TRAFFIC_PI0_BF16 = {"bytes_per_chunk": 6460884224,
+                    "kernel_sources_sha256": "c8e8d5dd90eec26374485a77e455b51ecab3a6ef9b7a3cfa9ed4961bf16f0e56"}
 
 
 def kernel_sources_sha256():
