@@ -14,8 +14,9 @@ of any strides with a dense last index and 16-byte steps.  Results are new
 tensors unless ``out`` is given.  Work goes to ``stream`` (a torch stream or
 its address), or to torch's current stream of the handle's GPU; results and
 workspaces are allocated for the stream that the work goes to, as if the call
-were made inside ``torch.cuda.stream(stream)``.  Outputs must not overlap
-inputs, and no gradient flows through the calls.
+were made inside ``torch.cuda.stream(stream)``, and tensors given to a call
+with a stream may be released at once.  Outputs must not overlap inputs, and
+no gradient flows through the calls.
 """
 
 from __future__ import annotations
@@ -81,6 +82,17 @@ class CacheOps:
     # ------------------------------------------------------------------
     def _on(self, stream):
         return on_stream(stream, self.device)
+
+    def _elsewhere(self, stream, call, *args):
+        """The call on that stream, whose queued work keeps the memory of what it is given."""
+        with self._on(stream):
+            result = call(*args)
+            used = torch.cuda.current_stream(self.device)
+            for a in args:
+                for t in a if isinstance(a, (tuple, list)) else (a,):
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(used)
+        return result
 
     def _stream(self) -> int:
         return torch._C._cuda_getCurrentRawStream(self.device)   # torch.cuda.current_stream without its object
@@ -200,8 +212,7 @@ class CacheOps:
         int32 tensor [B]; count: int32 tensor [B] of the tokens that are real
         (the rest is not written), or None."""
         if stream is not None:
-            with self._on(stream):
-                return self.write(cache, k, v, start, count)
+            return self._elsewhere(stream, self.write, cache, k, v, start, count)
         src, dst = self._rows(k, v, "k, v"), self._cache(cache, "cache")
         first, at = 0, None
         if isinstance(start, torch.Tensor):
@@ -216,8 +227,7 @@ class CacheOps:
         (n None: to the end) in dtype ("f32" or "bf16"), or into out = (k, v).
         Tokens at or past lens[b] (int32 [B]) read as zeros."""
         if stream is not None:
-            with self._on(stream):
-                return self.read(cache, n, first, lens, dtype, out)
+            return self._elsewhere(stream, self.read, cache, n, first, lens, dtype, out)
         src, first = self._cache(cache, "cache"), _place(first, "first")
         if out is None:
             n = src.n_tokens - first if n is None else n
@@ -238,8 +248,7 @@ class CacheOps:
         [B][N]).  scale None: D ** -0.5.  Returns out, or (out, lse) with lse
         True or a tensor [B][T][Hq]."""
         if stream is not None:
-            with self._on(stream):
-                return self.cross_attention(q, kv, lens, mask, scale, out, lse)
+            return self._elsewhere(stream, self.cross_attention, q, kv, lens, mask, scale, out, lse)
         desc, out, sums = self._queries(q, out, lse, scale)
         keys = self._cache(kv, "kv") if isinstance(kv, QuantizedKV) else self._rows(kv[0], kv[1], "kv")
         mp = self._bools(mask, "mask", (keys.batch, keys.n_tokens))
@@ -258,8 +267,8 @@ class CacheOps:
         if own is None and own_lens is not None:
             raise ValueError("own_lens without own keys")
         if stream is not None:
-            with self._on(stream):
-                return self.shared_attention(q, prefix, own, prefix_mask, own_lens, scale, out, lse)
+            return self._elsewhere(stream, self.shared_attention, q, prefix, own, prefix_mask, own_lens, scale, out,
+                                   lse)
         desc, out, sums = self._queries(q, out, lse, scale)
         pre = self._cache(prefix, "prefix") if isinstance(prefix, QuantizedKV) else \
             self._rows(prefix[0], prefix[1], "prefix", shared=True)

@@ -645,3 +645,21 @@ def test_values_near_the_least_exponents(ops, dtype, cache, tq, d):
     out, lse = ops.cross_attention(q, kv, lens=ints(lens), lse=True)
     kn, vn = f64(k), f64(v) / shrink
     check_attention(q, lambda i: [(kn[i], vn[i], visible(n, lens, None, i))], d ** -0.5, out.double() / shrink, lse)
+
+
+def test_tensors_given_with_a_stream_may_be_released_at_once(ops):
+    g = gen(36)
+    made = [rand(g, 2, 3, 8, 128), rand(g, 2, 500, 1, 128), rand(g, 2, 500, 1, 128), ints([500, 77])]
+    want = ops.cross_attention(made[0], made[1:3], lens=made[3])
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        given = [t.clone() for t in made]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                 # the call waits some 10 ms
+        got = ops.cross_attention(given[0], given[1:3], lens=given[3], stream=stream)
+        del given
+        for t in made:
+            torch.empty_like(t).fill_(1)                  # what was released serves again
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -116,3 +116,34 @@ def test_the_default_stream_is_the_contexts_gpus(world, monkeypatch):
     world.ex.denoise_shared(FakeTensor(world, (2, 5, 3), torch.float32, 17),
                             FakeTensor(world, (4,), torch.float32, 17), 2)
     assert [c[0][-1] for c in world.calls.values()] == [17, 17, 17]
+
+
+@pytest.mark.parametrize("stream,address", GIVEN[:2])
+def test_what_a_cache_operator_is_given_is_kept_until_its_stream_has_used_it(world, monkeypatch, stream, address):
+    from flow_matching_action_dm0_b200 import CacheOps, QuantizedKV
+    kept, went = [], []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: kept.append((id(self), s.cuda_stream)))
+    described = types.SimpleNamespace(batch=1, dtype=0, n_tokens=1, n_heads=1, head_dim=64)
+    for name in ("_rows", "_cache"):
+        monkeypatch.setattr(CacheOps, name, lambda self, *a, **kw: described)
+    monkeypatch.setattr(CacheOps, "_queries", lambda self, q, out, lse, scale: (described, out, lse))
+    monkeypatch.setattr(CacheOps, "_workspace", lambda self, *a: (None, 0, None))
+    for name in ("_ints", "_bools"):
+        monkeypatch.setattr(CacheOps, name, lambda self, *a: None)
+    monkeypatch.setattr(CacheOps, "_stream", lambda self: torch.cuda.current_stream(0).cuda_stream)
+    for name in ("rtv_kv_write", "rtv_kv_read", "rtv_cross_attention", "rtv_shared_attention"):
+        monkeypatch.setattr(L, name, lambda *a: went.append(a[-1]))
+    ops = object.__new__(CacheOps)
+    ops.device, ops.h, ops._torch_device = 0, None, torch.device("cuda", 0)
+    t = [torch.zeros(1) for _ in range(8)]
+    cache = QuantizedKV(*t[:4])
+    for call, given in ((lambda s: ops.write(cache, t[4], t[5], start=t[6], count=t[7], stream=s), t),
+                        (lambda s: ops.read(cache, lens=t[4], out=(t[5], t[6]), stream=s), t[:7]),
+                        (lambda s: ops.cross_attention(t[4], cache, lens=t[5], out=t[6], lse=t[7], stream=s), t),
+                        (lambda s: ops.shared_attention(t[0], (t[1], t[2]), (t[3], t[4]), prefix_mask=t[5],
+                                                        own_lens=t[6], out=t[7], stream=s), t)):
+        kept.clear()
+        call(stream())
+        assert went.pop() == address
+        assert sorted(kept) == sorted((id(x), address) for x in given)
+        assert len(world.current) == 1
